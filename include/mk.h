@@ -50,7 +50,7 @@ typedef enum {
                                 context is poisoned by an earlier device error */
 } mk_status;
 
-enum { MK_BF16 = 0 };
+enum { MK_BF16 = 0, MK_FP16 = 1, MK_FP32 = 2 }; /* mk_config.dtype: MK_BF16 only */
 /* Execution variants of one decode step. */
 enum {
     MK_MEGAKERNEL = 0, /* one persistent launch, tile-ready counters between ops */
@@ -102,7 +102,7 @@ typedef struct {
     int qk_norm;         /* 1: per-head RMSNorm of q and k before RoPE (Qwen3) */
     int batch;           /* sequences decoded together, 1..64 */
     int max_seq;         /* KV cache positions per sequence */
-    int dtype;           /* MK_BF16 (the only one) */
+    int dtype;           /* MK_BF16 (the only one here) */
     int variant;         /* MK_MEGAKERNEL | MK_GRAPH | MK_GRAPH_PDL | MK_GRAPH_TILESYNC | MK_TENSOR_CORES */
     int num_sms;         /* CTAs of the persistent kernel; 0 = the device's SM count */
 } mk_config;
@@ -475,6 +475,129 @@ mk_status mk_attention_decode_noalloc(const float *q, const void *k_cache, const
                                       float *out, void *stream);
 /* Bytes of the fixed scratch behind mk_attention_decode_noalloc (4 MiB). */
 size_t mk_attention_noalloc_limit_bytes(void);
+
+/* ---------------------------------------------------------------- paged cache
+ * A KV cache in pages, for what a serving loop does around the decoder: many
+ * sequences of any length in one pool, several new tokens per sequence and
+ * step (drafted trees, chunks of prompts, single tokens), sequences that share
+ * a prefix.  The cited articles have no counterpart of these entry points.
+ *
+ * A page holds page_size positions of one sequence, in every layer:
+ *   kv: device, [2][n_layers][n_pages][n_kv_heads][page_size][head_dim], K of
+ *       all layers, then V; MK_BF16 or MK_FP16.  A context's cache
+ *       (mk_kv_cache_bytes) is this layout with n_pages = batch and
+ *       page_size = max_seq, so these calls run on it too.
+ *   table: device int32 [max_seqs][max_pages]; entry j of a row is the page of
+ *       positions j * page_size ...; the entries in use are a prefix of the
+ *       row, the others are -1.
+ *   lengths: device int32 [max_seqs]: committed positions.  New tokens of a
+ *       step sit at positions length, length + 1, ... until mk_pages_compact
+ *       commits some of them.
+ *   refs: device int32 [n_pages]: sequences whose row holds the page; 0: free.
+ *   state: device, mk_pages_state_bytes(), zero-filled before first use.
+ * An empty pool is table -1, lengths 0, refs 0.  The caller owns all of it;
+ * the struct is read during the call only.
+ * Limits: head_dim in {64, 128, 256}; max_seqs <= 1024; n_pages <= 2^19;
+ * n_kv_heads <= 1024; n_layers <= 4096; page_size a multiple of 16, or any
+ * with max_pages = 1; max_pages * page_size <= 2^30; kv 16-byte aligned.
+ *
+ * Lists (`seqs`, `counts`, ...) are device int32 arrays, read when the call's
+ * kernels run, so captured calls follow their contents.  What only the device
+ * can see (an index out of range, a sequence listed twice, no free page, ...)
+ * leaves that entry undone and is recorded in `state`, the first one until
+ * mk_pages_status reads it; the other entries are done.  Calls that change a
+ * pool must be ordered with each other and with the calls that read it.  All
+ * are asynchronous on `stream` and allocate nothing.  Errors on the host:
+ * MK_ERR_INVALID, MK_ERR_UNSUPPORTED (head_dim, dtype, page_size),
+ * MK_ERR_CUDA; the reason is in mk_last_error(NULL). */
+typedef struct {
+    int n_layers, n_kv_heads, head_dim, page_size, n_pages;
+    int max_seqs, max_pages;
+    int dtype; /* MK_BF16 | MK_FP16 */
+    void *kv;
+    int32_t *table, *lengths, *refs, *state;
+} mk_pages;
+
+size_t mk_pages_state_bytes(void);
+/* Make room for counts[i] new tokens of sequence seqs[i], i < n: every
+ * position length .. length + counts[i] - 1 gets a page that the sequence
+ * holds alone.  A partly filled last page that another sequence holds too is
+ * copied first, in all layers (copy on write; of several listed sharers, each
+ * as long as another holder is left, in list order).  Pages are taken lowest
+ * index first, in list order; when the free ones do not suffice for the whole
+ * list, nothing is done. */
+mk_status mk_pages_reserve(const mk_pages *pages, const int32_t *seqs, const int32_t *counts, int n, void *stream);
+/* Sequence dst[i], empty, becomes a copy of src[i]'s committed positions by
+ * holding the same pages; no data moves.  A sequence may be forked several
+ * times in a call, but no dst may be a src or occur twice.  Reserve before the
+ * next new tokens of either, also where src had room reserved. */
+mk_status mk_pages_fork(const mk_pages *pages, const int32_t *src, const int32_t *dst, int n, void *stream);
+/* Commit new tokens: position length + j of sequence seqs[i] gets what
+ * position length + keep[i][j] holds, j < n_keep[i], in every layer, and the
+ * length grows by n_keep[i].  keep: [n][width], each row's first n_keep[i]
+ * entries ascending (the accepted path of a drafted tree), or NULL: the first
+ * n_keep[i] new tokens, in place (n_keep[i] is then not bounded by width).
+ * Pages behind the new length stay reserved. */
+mk_status mk_pages_compact(const mk_pages *pages, const int32_t *seqs, const int32_t *n_keep, const int32_t *keep,
+                           int width, int n, void *stream);
+/* Cut sequence seqs[i] to its first lengths[i] positions (NULL: 0) and give up
+ * the pages behind them, reserved ones included. */
+mk_status mk_pages_free(const mk_pages *pages, const int32_t *seqs, const int32_t *lengths, int n, void *stream);
+/* Page dst_pages[k] of `dst` = page src_pages[k] of `src`, in every layer: the
+ * same pool, or two with pages of the same shape and type (to move sequences
+ * between pools).  Tables and counts are not touched.  A pair is left out when
+ * its destination occurs twice or, within one pool, its source is written by
+ * the same call. */
+mk_status mk_pages_copy(const mk_pages *dst, const mk_pages *src, const int32_t *src_pages, const int32_t *dst_pages,
+                        int n, void *stream);
+/* The first error the pool's kernels recorded since the last call, which
+ * clears it: MK_OK, MK_ERR_INVALID, MK_ERR_STATE (not enough free pages) or
+ * MK_ERR_TIMEOUT, with the reason in mk_last_error(NULL).  Waits for `stream`. */
+mk_status mk_pages_status(const mk_pages *pages, void *stream);
+
+/* The pass from the QKV projection to the attention: RMSNorm of every q and k
+ * head (with gains), rotation by each token's own position, q in the cache's
+ * type, K and V into the pages.  Token t < n_new[i] of entry i (sequence
+ * seqs[i]) is written at position length + t and rotated by
+ * length + depth[i][t]:
+ *   x' = x / sqrt(mean(x^2) + eps) * gain      (NULL gain: x' = x),
+ *   (x'_j, x'_{j+d/2}) turned by (length + depth) * theta^(-2j/d), j < d/2.
+ * qkv: device, MK_FP32 or the cache's type, token (i, t) at
+ * qkv + (i T + t) * qkv_stride (elements): n_heads q heads, then the k heads,
+ * then the v heads (the row of mk_linear_tc on stacked weights).  n_new: NULL
+ * = T for all; tokens t >= n_new[i] are padding, nothing of theirs is written.
+ * depth: [n][T] (a token's depth in its tree), NULL = t.  gains: bf16
+ * [head_dim] or NULL.  q: token (i, t) at q + (i T + t) * q_stride.  Strides
+ * are multiples of 8, pointers 16-byte aligned.  A sequence may occur once.
+ * A slot without a page, or in a page held by another sequence too, is not
+ * written (mk_pages_status tells). */
+mk_status mk_qk_norm_rope(const mk_pages *pages, int layer, const void *qkv, int qkv_dtype, long long qkv_stride,
+                          int n, int T, int n_heads, const int32_t *seqs, const int32_t *n_new, const int32_t *depth,
+                          const void *q_gain, const void *k_gain, float eps, double theta, void *q,
+                          long long q_stride, void *stream);
+
+/* Attention of the new tokens over the pages of one layer: token t < n_new[i]
+ * of entry i sees the length committed positions of sequence seqs[i] and the
+ * new tokens u < n_new[i] with bit u of its mask row set:
+ *   out[i][t][h] = sum_j softmax_j(q[i][t][h] . K[g][j] / sqrt(d)) V[g][j],
+ *   g = h / (n_heads / n_kv_heads).
+ * mask: device uint32 [n][T][(T + 31) / 32], bit u % 32 of word u / 32 (a
+ * tree: a token's ancestors and itself); NULL: u <= t (a chunk of a prompt;
+ * T = 1: a decode step).  A row that sees nothing is 0.  An infinity or NaN in
+ * K or V at a position that a row does not see does not reach it.  Rows
+ * t >= n_new[i] of out are left as they were.  q, out: the cache's type, token
+ * (i, t) at (i T + t) * stride elements (multiples of 8), n_heads x head_dim
+ * values each, 16-byte aligned; out must not overlap q.  A sequence may occur
+ * several times; n <= 1024.
+ * scratch: device, mk_attention_tree_scratch_bytes (for the current device's
+ * SM count), 16-byte aligned, needs no initialisation; calls that share it
+ * must not overlap.  Results do not depend on it.  32-bit scores, softmax and
+ * sums; P enters the second product in the cache's 16-bit type.  A device-side
+ * wait that runs out (2 s) writes NaN and is reported by mk_pages_status. */
+mk_status mk_attention_tree(const mk_pages *pages, int layer, const void *q, long long q_stride, int n, int T,
+                            int n_heads, const int32_t *seqs, const int32_t *n_new, const uint32_t *mask, void *out,
+                            long long out_stride, void *scratch, size_t scratch_bytes, void *stream);
+size_t mk_attention_tree_scratch_bytes(int T, int n_heads, int n_kv_heads, int head_dim);
 
 #ifdef __cplusplus
 }

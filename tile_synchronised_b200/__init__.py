@@ -13,8 +13,10 @@ import torch
 from ._lib import (MK_GRAPH, MK_GRAPH_PDL, MK_GRAPH_TILESYNC, MK_MEGAKERNEL, MK_TENSOR_CORES, MK_SWIGLU_AUTO, MK_SWIGLU_COL, MK_SWIGLU_ROW,
                    MK_SWIGLU_TC, MK_SYNC_COUNTERS, MK_SYNC_TAGS, MkConfig, MkError, MkWeights, check, load)
 
+from .paged import PagedCache, attention_tree, qk_norm_rope, tree_mask  # noqa: F401
+
 __all__ = ["Model", "TcDecoder", "swiglu_stage1", "swiglu_tune", "linear_tc", "linear_tc_split", "MkError", "VARIANTS",
-           "MK_SWIGLU_AUTO", "MK_SWIGLU_ROW", "MK_SWIGLU_COL", "MK_SWIGLU_TC", "load"]
+           "PagedCache", "qk_norm_rope", "attention_tree", "tree_mask", "MK_SWIGLU_AUTO", "MK_SWIGLU_ROW", "MK_SWIGLU_COL", "MK_SWIGLU_TC", "load"]
 
 VARIANTS = {"megakernel": MK_MEGAKERNEL, "graph": MK_GRAPH, "graph_pdl": MK_GRAPH_PDL, "tilesync": MK_GRAPH_TILESYNC,
             "tensor_cores": MK_TENSOR_CORES}

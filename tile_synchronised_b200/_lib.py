@@ -11,7 +11,7 @@ import os
 from . import build as _build
 
 MK_OK, MK_ERR_INVALID, MK_ERR_CUDA, MK_ERR_TIMEOUT, MK_ERR_UNSUPPORTED, MK_ERR_STATE = 0, -1, -2, -3, -4, -5
-MK_BF16 = 0
+MK_BF16, MK_FP16, MK_FP32 = 0, 1, 2
 MK_MEGAKERNEL, MK_GRAPH, MK_GRAPH_PDL, MK_GRAPH_TILESYNC, MK_TENSOR_CORES = 0, 1, 2, 3, 4
 MK_SWIGLU_AUTO, MK_SWIGLU_ROW, MK_SWIGLU_COL, MK_SWIGLU_TC = 0, 1, 2, 3
 MK_SYNC_TAGS, MK_SYNC_COUNTERS = 0, 1
@@ -32,7 +32,10 @@ EXPORTS = ("mk_create", "mk_destroy", "mk_last_error", "mk_workspace_bytes", "mk
            "mk_attention_decode_noalloc", "mk_attention_noalloc_limit_bytes", "mk_linear_tc",
            "mk_linear_tc_split", "mk_linear_tc_streamk", "mk_linear_tc_streamk_workspace_bytes",
            "mk_linear_tc_streamk_grid", "mk_tcdec_create", "mk_tcdec_workspace_bytes", "mk_tcdec_bind", "mk_tcdec_step",
-           "mk_tcdec_status", "mk_tcdec_last_error", "mk_tcdec_destroy", "mk_tcdec_set_graph")
+           "mk_tcdec_status", "mk_tcdec_last_error", "mk_tcdec_destroy", "mk_tcdec_set_graph",
+           "mk_pages_state_bytes", "mk_pages_reserve", "mk_pages_fork", "mk_pages_compact", "mk_pages_free",
+           "mk_pages_copy", "mk_pages_status", "mk_qk_norm_rope", "mk_attention_tree",
+           "mk_attention_tree_scratch_bytes")
 
 
 class MkConfig(C.Structure):
@@ -50,6 +53,12 @@ class MkWeights(C.Structure):
     _fields_ = [("embed", C.c_void_p), ("final_norm", C.c_void_p), ("lm_head", C.c_void_p)] + \
                [(n, _PP) for n in ("attn_norm", "wq", "wk", "wv", "wo", "q_norm", "k_norm", "mlp_norm",
                                    "wg", "wu", "wd")]
+
+
+class MkPages(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("n_layers", "n_kv_heads", "head_dim", "page_size", "n_pages", "max_seqs",
+                                       "max_pages", "dtype")] + \
+               [(n, C.c_void_p) for n in ("kv", "table", "lengths", "refs", "state")]
 
 
 class MkError(RuntimeError):
@@ -74,7 +83,7 @@ def load() -> C.CDLL:
             raise RuntimeError(f"libmk.so is missing and could not be built: {e}") from e
     L = C.CDLL(path)
     vp, i32, sz = C.c_void_p, C.c_int, C.c_size_t
-    st = C.c_int
+    st, ll, pg = C.c_int, C.c_longlong, C.POINTER(MkPages)
     sig = {
         "mk_create": ([C.POINTER(MkConfig), i32, C.POINTER(vp)], st),
         "mk_destroy": ([vp], st),
@@ -125,6 +134,17 @@ def load() -> C.CDLL:
         "mk_tcdec_last_error": ([vp], C.c_char_p),
         "mk_tcdec_destroy": ([vp], st),
         "mk_tcdec_set_graph": ([vp, i32], st),
+        "mk_pages_state_bytes": ([], sz),
+        "mk_pages_reserve": ([pg, vp, vp, i32, vp], st),
+        "mk_pages_fork": ([pg, vp, vp, i32, vp], st),
+        "mk_pages_compact": ([pg, vp, vp, vp, i32, i32, vp], st),
+        "mk_pages_free": ([pg, vp, vp, i32, vp], st),
+        "mk_pages_copy": ([pg, pg, vp, vp, i32, vp], st),
+        "mk_pages_status": ([pg, vp], st),
+        "mk_qk_norm_rope": ([pg, i32, vp, i32, ll, i32, i32, i32, vp, vp, vp, vp, vp, C.c_float, C.c_double, vp, ll,
+                             vp], st),
+        "mk_attention_tree": ([pg, i32, vp, ll, i32, i32, i32, vp, vp, vp, vp, ll, vp, sz, vp], st),
+        "mk_attention_tree_scratch_bytes": ([i32, i32, i32, i32], sz),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)

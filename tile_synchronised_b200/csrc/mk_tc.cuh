@@ -150,5 +150,11 @@ bool tc_make_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols,
 // out in shared memory exactly as a 2-D box of a row-major matrix, 128-byte
 // swizzled.  kc a multiple of 64, rows a power of two <= 128.
 bool tc_make_map_packed(CUtensorMap *m, const void *base, uint64_t tiles, uint32_t nkb, uint32_t rows, uint32_t kc);
+// One layer's K or V pages, [rows][page_size][d] 2-byte elements (rows = pages x
+// KV heads, d a multiple of 64), as a 4-D tensor (64 columns, page_size,
+// d / 64, rows) with a box of 64 x `positions` x `blocks` x 1, 128-byte
+// swizzled: `blocks` K-major operand blocks of 64 columns, one behind the other.
+bool tc_make_map_pages(CUtensorMap *m, const void *base, uint64_t rows, uint32_t page_size, uint32_t d,
+                       uint32_t positions, uint32_t blocks);
 
 }  // namespace mk
