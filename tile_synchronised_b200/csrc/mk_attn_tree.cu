@@ -8,16 +8,25 @@
 //   a mask).
 //
 // The T new tokens of the G = nq / nkv query heads that share a KV head are
-// the rows of one matrix (row r = t G + g), up to 128 of them the M of an MMA,
-// so the cache is read once for all of them and the arithmetic (4 d flops per
-// row and position) stays behind the memory traffic (4 d bytes per position)
-// for up to about 250 rows.  Per tile of NT positions:
+// the rows of one matrix (row r = t G + g), 128 of them the M of an MMA, so the
+// cache is read once for up to 256 rows and the arithmetic (4 d flops per row
+// and position) stays behind the memory traffic (4 d bytes per position).  Per
+// tile of NT positions:
 //     S = Q K^T  (tensor memory, M = 128, N = NT), softmax in registers,
 //     P (16 bit, tensor memory, over S) and O += P V (tensor memory, N = d).
 // One thread owns one row of S, so the running maximum and sum need no
-// exchange.  O is rescaled only when the maximum grew by more than 2^8 since
-// the last rescale: P and the sum then stay within 32-bit range of the older
-// maximum and the quotient is the same.
+// exchange.  It holds 32 or 64 of the scores at a time: with more in registers
+// the compiler spills, and with 227 KB of the SM given to the operands there is
+// hardly an L1 to spill to (scores all in registers: 2.4 times slower).  O is
+// rescaled only when the maximum grew by more than 2^8 since the last rescale:
+// P and the sum then stay within 32-bit range of the older maximum and the
+// quotient is the same.
+//
+// The softmax of a tile takes a group of four warps about as long as its K and
+// V take to arrive, so (d <= 128) two groups work, each with an S and an O of
+// its own.  Up to 128 rows they take alternate tiles of positions and their
+// results are joined at the end of a run; above, they take 128 rows each of
+// every tile.  At d = 256 tensor memory holds one O: one group, two S.
 //
 // Work: the units are (sequence, KV head, row tile, tile of positions), the
 // tiles of one row tile consecutive; each CTA (one per SM) takes an equal
@@ -26,10 +35,10 @@
 // writes (o, max, sum) to scratch, at most two such records per CTA, and
 // tree_combine_kernel joins them.
 //
-// Roles: warps 0-3 softmax (thread = row), one warp loads K and V tiles by
-// TMA into a ring (a page's share of a tile per copy; lanes look up the page
-// table two tiles ahead), one lane issues the MMAs: QK of the next tile goes
-// out before PV of this one, so the tensor core works while the softmax runs.
+// Roles: the softmax warps; one warp loads K and V tiles by TMA
+// into a ring (a page's share of a tile per copy; the lanes look up 32 pages
+// at a time, ahead); one lane issues the MMAs: with two jobs (tile, group) in
+// flight, S of job j + 2 follows P V of job j.
 //
 // P is rounded to the cache's 16-bit type (2^-9 relative in bf16, each
 // element on its own, as V's own storage); S, the maximum, the sum, O and the
@@ -49,6 +58,12 @@ namespace mk {
 constexpr int kTreeM = 128;          // rows of an MMA
 constexpr int kTreeMaxStages = 12;
 
+// Softmax groups, positions of a tile and rows of an item at head size d.
+__host__ __device__ constexpr int tree_groups(int d) { return d == 256 ? 1 : 2; }
+__host__ __device__ constexpr int tree_nt(int d) { return d == 256 ? 64 : 128; }
+__host__ __device__ constexpr int tree_rows(int d) { return kTreeM * tree_groups(d); }
+__host__ __device__ constexpr int tree_threads(int d) { return (4 * tree_groups(d) + 2) * 32; }
+
 struct TreeArgs {
     mk_pages p;
     const uint16_t *q;
@@ -56,67 +71,80 @@ struct TreeArgs {
     long long q_stride, out_stride;  // 16-bit elements between tokens
     const int *seqs, *n_new;
     const uint32_t *mask;
-    float *part_o;   // [2 x CTAs][rows_cap][d]
+    float4 *part_o;  // [2 x CTAs][d / 4][rows_cap]: rows side by side, as the threads that write them
     float2 *part_ml; // [2 x CTAs][rows_cap]: maximum (base 2, scaled), sum
     const uint16_t *k, *v;  // this layer's pages
-    int n, T, words, nq, G, seg, stages, rows_cap;
+    int n, T, words, nq, G, seg, stages, q_tiles, rows_cap;
     float scale;     // log2(e) / sqrt(d)
 };
 
-// What one listed sequence needs: units, and the walk over a CTA's range.
+// A listed sequence.
 struct TreeEntry {
     int seq, len, fresh;
 };
 
-__host__ __device__ constexpr int tree_nt(int d) { return d == 256 ? 64 : 128; }
+// A run of tiles of one item that one CTA works through, and where the walk
+// over the CTA's range of units is; each warp has its own.
+struct TreeRun {
+    int i, g, rt, t0, t1, tiles, slot, more;
+    TreeEntry e;
+    int count;
+    long long u, u1;
+};
 
 // Shared memory behind the operand tiles.
 struct TreeShared {
     uint64_t full[kTreeMaxStages], empty[kTreeMaxStages];
-    uint64_t s_full[2], p_full[2], pv_done, q_full;
+    uint64_t s_full[2], p_full[2], pv_done[2], q_full;
+    TreeRun run[10];       // of each warp
+    float2 ml[2][kTreeM];  // the groups' maxima (scaled) and sums at the end of a run
     uint32_t tmem;
     int abort, bad_v, pad;
 };
 
 // The units of entry e: KV heads x row tiles x tiles of positions.
-__device__ __forceinline__ long long tree_units(const TreeArgs &a, const TreeEntry &e, int nt) {
+template <int D>
+__device__ __forceinline__ long long tree_units(const TreeArgs &a, const TreeEntry &e) {
     if (!e.fresh) return 0;
-    const int rt = (e.fresh * a.G + kTreeM - 1) / kTreeM, tiles = (e.len + e.fresh + nt - 1) / nt;
-    return (long long)a.p.n_kv_heads * rt * tiles;
+    const int rts = (e.fresh * a.G + tree_rows(D) - 1) / tree_rows(D), tiles = (e.len + e.fresh + tree_nt(D) - 1) / tree_nt(D);
+    return (long long)a.p.n_kv_heads * rts * tiles;
 }
 
-// A run of tiles of one item that one CTA works through.
-struct TreeSeg {
-    int i, g, rt, t0, t1, tiles, slot;
-    TreeEntry e;
-};
+// n / d, mostly of small numbers (a 64-bit division takes hundreds of cycles).
+__device__ __forceinline__ long long small_div(long long n, int d) {
+    return n >> 32 ? n / d : (long long)((uint32_t)n / (uint32_t)d);
+}
 
-struct TreeWalk {
-    long long u, u1;
-    int i, count;
-    const long long *pref;  // [n + 1] units before each entry
-    const TreeEntry *ent;
-    // the next run, false at the end of the CTA's range
-    __device__ __forceinline__ bool next(const TreeArgs &a, int nt, TreeSeg &s) {
-        if (u >= u1) return false;
-        while (pref[i + 1] <= u) ++i;
-        s.i = i;
-        s.e = ent[i];
-        s.tiles = (s.e.len + s.e.fresh + nt - 1) / nt;
-        const int rts = (s.e.fresh * a.G + kTreeM - 1) / kTreeM;
-        const long long local = u - pref[i];
-        const int item = (int)(local / s.tiles);
-        s.t0 = (int)(local - (long long)item * s.tiles);
-        s.g = item / rts;
-        s.rt = item - s.g * rts;
-        const long long left = u1 - u;
-        s.t1 = left < s.tiles - s.t0 ? s.t0 + (int)left : s.tiles;
-        s.slot = 2 * blockIdx.x + (count ? 1 : 0);
-        ++count;
-        u += s.t1 - s.t0;
-        return true;
+// The warp's next run, false at the end of the CTA's range.
+template <int D>
+__device__ __forceinline__ bool tree_next(const TreeArgs &a, TreeRun &r, const long long *pref, const TreeEntry *ent) {
+    constexpr int nt = tree_nt(D);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+        r.more = r.u < r.u1;
+        if (r.more) {
+            int i = r.i;
+            while (pref[i + 1] <= r.u) ++i;
+            const TreeEntry e = ent[i];
+            r.i = i;
+            r.e = e;
+            r.tiles = (e.len + e.fresh + nt - 1) / nt;
+            const int rts = (e.fresh * a.G + tree_rows(D) - 1) / tree_rows(D);
+            const long long local = r.u - pref[i];
+            const int item = (int)small_div(local, r.tiles);
+            r.t0 = (int)(local - (long long)item * r.tiles);
+            r.g = item / rts;
+            r.rt = item - r.g * rts;
+            const long long left = r.u1 - r.u;
+            r.t1 = left < r.tiles - r.t0 ? r.t0 + (int)left : r.tiles;
+            r.slot = 2 * blockIdx.x + (r.count ? 1 : 0);
+            r.count = 1;
+            r.u += r.t1 - r.t0;
+        }
     }
-};
+    __syncwarp();
+    return r.more;
+}
 
 // The CTAs that share U units out of `most`: at least kTreeMinUnits each.
 constexpr int kTreeMinUnits = 2;
@@ -124,7 +152,7 @@ __device__ __forceinline__ int tree_ctas(long long U, int most) {
     const long long want = (U + kTreeMinUnits - 1) / kTreeMinUnits;
     return want < most ? (int)(want > 0 ? want : 1) : most;
 }
-__device__ __forceinline__ long long tree_first(long long U, int ctas, int c) { return U * c / ctas; }
+__device__ __forceinline__ long long tree_first(long long U, int ctas, int c) { return small_div(U * c, ctas); }
 
 // 32 visibility bits of row `row` (a new token) for new tokens 32 k .. 32 k + 31
 // (k < 0: committed positions, all visible).
@@ -165,15 +193,41 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
+// Waits for this thread's tensor-memory loads.  The loaded registers are
+// operands, so that no use of them can be moved above the wait.
+__device__ __forceinline__ void tmem_wait_ld(float *v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                   "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]),
+                   "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
+                   "+f"(v[30]), "+f"(v[31])
+                 :
+                 : "memory");
+}
+// 16 columns (no wait), and the wait for them.
+__device__ __forceinline__ void tmem_ld16n(uint32_t taddr, float *v) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld16(float *v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]),
+                   "+f"(v[15])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(taddr),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -208,44 +262,134 @@ __device__ __forceinline__ bool any_nonfinite(const uint4 &v) {
     return bad;
 }
 
-// The share of new tokens whose V holds an infinity or NaN.  In the MMA those
-// rows of V are zeros, since 0 x inf in a row that does not see the token
-// would be NaN; here every row that does see one adds p V itself, columns
-// c0 .. c0 + 31.  Rarely runs.
-template <int D, bool BF16>
-__device__ __noinline__ void tree_add_nonfinite(const TreeArgs &a, const TreeSeg &s, int nt, int row, float m2,
-                                                float bias, int c0, float *o) {
-    const int t = row / a.G;
-    const uint16_t *q = a.q + ((size_t)s.i * a.T + t) * a.q_stride + (size_t)(s.g * a.G + row % a.G) * D;
-    const int from = max(s.e.len, s.t0 * nt), to = min(s.e.len + s.e.fresh, s.t1 * nt);
-    for (int pos = from; pos < to; ++pos) {
-        if (!(tree_bits(a, s.i, t, s.e, pos) & 1u)) continue;
-        const int page = a.p.table[(size_t)s.e.seq * a.p.max_pages + pos / a.p.page_size];
-        if (page < 0 || page >= a.p.n_pages) continue;
-        const size_t at = (((size_t)page * a.p.n_kv_heads + s.g) * a.p.page_size + pos % a.p.page_size) * D;
-        bool bad = false;
-        for (int c = 0; c < D; c += 8) bad = bad || any_nonfinite<BF16>(*reinterpret_cast<const uint4 *>(a.v + at + c));
-        if (!bad) continue;
-        float dot = 0.f;
-        for (int c = 0; c < D; ++c) dot = fmaf(from16<BF16>(q[c]), from16<BF16>(a.k[at + c]), dot);
-        const float p = ex2(fmaf(dot, a.scale, bias - m2));
-        for (int c = 0; c < 32; ++c) o[c] = fmaf(p, from16<BF16>(a.v[at + c0 + c]), o[c]);
+// Packed pairs of 32-bit floats.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &x, float &y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+
+// True in one lane of the warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// The barrier of the softmax threads.
+template <int NG>
+__device__ __forceinline__ void softmax_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(NG * 128) : "memory");
+}
+
+// What a thread writes at the end of a run: columns c0 .. c1 - 1 of its row.
+struct TreeOut {
+    uint32_t o_mine, o_other;  // tensor memory of the group's O and of the other's (0: not read)
+    float f0, f1;              // their weights
+    float inv;                 // 1 / sum for the result, 1 for a record
+    float m2, bias;
+    int c0, c1, row, t;
+    bool mine, live, whole, ok;
+    float4 *rec;
+    uint16_t *to;
+};
+
+// With ADD also the share of new tokens whose V holds an infinity or NaN.  In
+// the MMA those rows of V are zeros, since 0 x inf in a row that does not see
+// the token would be NaN; here every row that does see one adds p V itself.
+template <int D, bool BF16, bool ADD>
+__device__ __forceinline__ void tree_write(const TreeArgs &a, const TreeRun &r, const TreeOut &w) {
+    for (int c = w.c0; c < w.c1; c += 16) {
+        float o[16], x[16];
+        if (w.mine && w.ok) {
+            tmem_ld16n(w.o_mine + c, o);
+            tmem_wait_ld16(o);
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[k] = !w.ok ? CUDART_NAN_F : w.mine ? o[k] * w.f0 : 0.f;
+        if (w.o_other && w.ok) {
+            tmem_ld16n(w.o_other + c, x);
+            tmem_wait_ld16(x);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = fmaf(x[k], w.f1, o[k]);
+        }
+        if (w.live) {
+            if constexpr (ADD) {
+                const uint16_t *q = a.q + ((size_t)r.i * a.T + w.t) * a.q_stride + (size_t)(r.g * a.G + w.row - w.t * a.G) * D;
+                const int to = min(r.e.len + r.e.fresh, r.t1 * tree_nt(D));
+                for (int pos = max(r.e.len, r.t0 * tree_nt(D)); pos < to; ++pos) {
+                    if (!(tree_bits(a, r.i, w.t, r.e, pos) & 1u)) continue;
+                    const int page = a.p.table[(size_t)r.e.seq * a.p.max_pages + pos / a.p.page_size];
+                    if (page < 0 || page >= a.p.n_pages) continue;
+                    const size_t at = (((size_t)page * a.p.n_kv_heads + r.g) * a.p.page_size + pos % a.p.page_size) * D;
+                    bool bad = false;
+                    for (int k = 0; k < D; k += 8)
+                        bad = bad || any_nonfinite<BF16>(*reinterpret_cast<const uint4 *>(a.v + at + k));
+                    if (!bad) continue;
+                    float dot = 0.f;
+                    for (int k = 0; k < D; ++k) dot = fmaf(from16<BF16>(q[k]), from16<BF16>(a.k[at + k]), dot);
+                    const float p = ex2(fmaf(dot, a.scale, w.bias - (w.m2 == -CUDART_INF_F ? 0.f : w.m2)));
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) o[k] = fmaf(p, from16<BF16>(a.v[at + c + k]), o[k]);
+                }
+            }
+            if (w.whole) {
+#pragma unroll
+                for (int k = 0; k < 16; k += 8) {
+                    uint4 v;
+                    v.x = pack16<BF16>(o[k] * w.inv, o[k + 1] * w.inv);
+                    v.y = pack16<BF16>(o[k + 2] * w.inv, o[k + 3] * w.inv);
+                    v.z = pack16<BF16>(o[k + 4] * w.inv, o[k + 5] * w.inv);
+                    v.w = pack16<BF16>(o[k + 6] * w.inv, o[k + 7] * w.inv);
+                    *reinterpret_cast<uint4 *>(w.to + c + k) = v;
+                }
+            } else {
+                float4 *rec = w.rec + (size_t)(c / 4) * a.rows_cap;
+#pragma unroll
+                for (int k = 0; k < 16; k += 4)
+                    rec[(size_t)(k / 4) * a.rows_cap] = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+            }
+        }
+        __syncwarp();
     }
+}
+template <int D, bool BF16>
+__device__ __noinline__ void tree_write_add(const TreeArgs &a, const TreeRun &r, const TreeOut &w) {
+    tree_write<D, BF16, true>(a, r, w);
 }
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(192, 1)
+__global__ void __launch_bounds__(tree_threads(D), 1)
     attn_tree_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                     const TreeArgs a) {
-    constexpr int NT = tree_nt(D), NH = D / 64;      // positions of a tile, 64-column blocks of a row
+                     const __grid_constant__ TreeArgs a) {
+    constexpr int NT = tree_nt(D), NH = D / 64;  // positions of a tile, 64-column blocks of a row
+    constexpr int NG = tree_groups(D), kLoader = 4 * NG, kIssuer = kLoader + 1;
     constexpr uint32_t kQBytes = kTreeM * D * 2, kStage = NT * D * 2;
-    constexpr uint32_t kO = 256;                      // tensor-memory column of O; S at 0 and 128
-    constexpr float kBias = BF16 ? 0.f : 7.f;         // fp16 P: 2^7 above the maximum's 1, so that small
-                                                      // values keep clear of its subnormals (at most 2^15)
-    constexpr float kGrow = 8.f;                      // rescale O when the maximum grew by more (base 2)
+    constexpr uint32_t kO = 256;                  // tensor-memory column of the first O; S at 0 and 128
+    constexpr float kBias = BF16 ? 0.f : 7.f;     // fp16 P: 2^7 above the maximum's 1, so that small
+                                                  // values keep clear of its subnormals (at most 2^15)
+    constexpr float kGrow = 8.f;                  // rescale O when the maximum grew by more (base 2)
     extern __shared__ __align__(1024) uint8_t tree_smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(tree_smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *s_q = smem, *ring = smem + kQBytes;
+    uint8_t *s_q = smem, *ring = smem + a.q_tiles * kQBytes;
     const int S = a.stages;
     TreeShared &sh = *reinterpret_cast<TreeShared *>(ring + (size_t)S * kStage);
     long long *pref = reinterpret_cast<long long *>(&sh + 1);
@@ -261,25 +405,27 @@ __global__ void __launch_bounds__(192, 1)
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sh.s_full[s], 1);
             mbar_init(&sh.p_full[s], 4);
+            mbar_init(&sh.pv_done[s], 1);
         }
-        mbar_init(&sh.pv_done, 1);
-        mbar_init(&sh.q_full, 4);
+        mbar_init(&sh.q_full, 4 * NG);
         sh.abort = 0;
         sh.bad_v = 0;
         fence_barrier_init();
     }
-    if (warp == 5) {
+    if (warp == kIssuer) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)),
                      "r"(512u)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    if (warp == kLoader && lane < 2)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &map_v : &map_k) : "memory");
     // the listed sequences and the units before each
     for (int i = tid; i < a.n; i += blockDim.x) {
         const PagesEntry e = pages_entry(a.p, a.seqs, a.n_new, i, a.T);
         if (e.err && blockIdx.x == 0) pages_fail(a.p.state, e.err, i, e.seq);
         ent[i] = TreeEntry{e.seq, e.len, e.fresh};
-        pref[i + 1] = tree_units(a, ent[i], NT);
+        pref[i + 1] = tree_units<D>(a, ent[i]);
     }
     tc_fence_before();
     __syncthreads();
@@ -301,49 +447,58 @@ __global__ void __launch_bounds__(192, 1)
     __syncthreads();
     pdl_launch_dependents();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&sh.tmem);
-    const long long U = pref[a.n];
-    const int ctas = tree_ctas(U, gridDim.x);
-    TreeWalk walk{0, 0, 0, 0, pref, ent};
-    if ((int)blockIdx.x < ctas) {
-        walk.u = tree_first(U, ctas, blockIdx.x);
-        walk.u1 = tree_first(U, ctas, blockIdx.x + 1);
+    TreeRun &run = sh.run[warp];
+    if (lane == 0) {
+        const long long U = pref[a.n];
+        const int ctas = tree_ctas(U, gridDim.x);
+        const bool mine = (int)blockIdx.x < ctas;
+        run.u = mine ? tree_first(U, ctas, blockIdx.x) : 0;
+        run.u1 = mine ? tree_first(U, ctas, blockIdx.x + 1) : 0;
         int lo = 0, hi = a.n;  // the last entry that starts at or before u
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
-            if (pref[mid] <= walk.u)
+            if (pref[mid] <= run.u)
                 lo = mid;
             else
                 hi = mid;
         }
-        walk.i = lo;
+        run.i = lo;
+        run.count = 0;
     }
-    TreeSeg sg;
-    int issued = 0;  // ring loads the producer issued
+    int issued = 0;  // ring loads the loader issued
+    // Jobs of a run, in order: with two row tiles (both groups on every tile)
+    // job j is group j & 1 of tile j / 2, else S buffer j & 1 of tile j.
+    auto two_rows = [&]() { return NG == 2 && run.e.fresh * a.G - run.rt * tree_rows(D) > kTreeM; };
 
-    if (warp == 4) {
-        // ---------------------------------------------------------- producer
-        const int seg = a.seg, ns = NT / seg;
+    if (warp == kLoader) {
+        // ------------------------------------------------------------ loader
+        const int seg = a.seg, ns = NT / seg, per = 32 / ns;
         const int nh = ns > 1 ? NH : 1;  // a whole tile's box covers every 64-column block
         const int my = lane / nh, blk = lane - my * nh;
         const int nkv = a.p.n_kv_heads, ps = a.p.page_size;
         const uint32_t seg_bytes = (uint32_t)seg * D * 2, off_smem = (uint32_t)(blk * NT + my * seg) * 128u;
         bool ok = true;
-        while (ok && walk.next(a, NT, sg)) {
-            const int *row = a.p.table + (size_t)sg.e.seq * a.p.max_pages;
-            const int end = sg.e.len + sg.e.fresh;
+        while (ok && tree_next<D>(a, run, pref, ent)) {
+            const int *row = a.p.table + (size_t)run.e.seq * a.p.max_pages;
+            const int end = run.e.len + run.e.fresh, t1 = run.t1, g = run.g;
             const bool mine = lane < ns * nh;
-            auto look = [&](int t) {
-                const int pos = t * NT + my * seg;
-                return mine && t < sg.t1 && pos < end ? row[pos / ps] : -1;
+            // lane x holds the page of part x % ns of tile tb + x / ns
+            auto look = [&](int tb) {
+                const int t = tb + lane / ns, pos = t * NT + lane % ns * seg;
+                return t < t1 && pos < end ? row[pos / ps] : -1;
             };
-            int p0 = look(sg.t0), p1 = look(sg.t0 + 1);
-            for (int t = sg.t0; ok && t < sg.t1; ++t) {
-                const int p2 = look(t + 2);
+            int tb = run.t0, pages = look(tb), next = look(tb + per);
+            for (int t = tb; ok && t < t1; ++t) {
+                if (t - tb == per) {
+                    tb = t;
+                    pages = next;
+                    next = look(tb + per);
+                }
+                int page = __shfl_sync(0xFFFFFFFFu, pages, ((t - tb) * ns + my) & 31);
                 const int pos = t * NT + my * seg, off = pos - pos / ps * ps;
                 const bool go = mine && pos < end;
-                int page = p0;
                 if (go && (page < 0 || page >= a.p.n_pages)) {
-                    pages_fail(a.p.state, kPgPosition, sg.i, pos);
+                    pages_fail(a.p.state, kPgPosition, run.i, pos);
                     page = -1;  // out of the tensor: zeros
                 }
                 const int left = (end - t * NT + seg - 1) / seg;
@@ -359,268 +514,336 @@ __global__ void __launch_bounds__(192, 1)
                     __syncwarp();
                     if (go)
                         tma_load_4d(ring + (size_t)s * kStage + off_smem, kv ? &map_v : &map_k, 0, off, blk,
-                                    page < 0 ? -1 : page * nkv + sg.g, &sh.full[s]);
+                                    page < 0 ? -1 : page * nkv + g, &sh.full[s]);
                     ++issued;
                 }
-                p0 = p1;
-                p1 = p2;
             }
         }
-    } else if (warp == 5) {
+    } else if (warp == kIssuer) {
         // -------------------------------------------------------- MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t id_qk = tree_idesc<BF16>(NT, false), id_pv = tree_idesc<BF16>(D, true);
-            int load = 0, tau = 0, seg_no = 0;  // ring loads used, tiles, runs
-            bool ok = true;
-            auto qk = [&](int x, int ld) {
-                const int s = ld % S;
-                if (!tc_wait(&sh.full[s], (ld / S) & 1u, abort)) return false;
+        constexpr uint32_t id_qk = tree_idesc<BF16>(NT, false), id_pv = tree_idesc<BF16>(D, true);
+        // descriptors of the first 16 columns (positions); a step of 16 adds
+        // 32 bytes along a row (16 rows), in units of 16 bytes
+        const uint64_t d_q = smem_desc_sw128(s_q, 16, 1024), d_k = smem_desc_sw128(ring, 16, 1024),
+                       d_v = smem_desc_sw128(ring, NT * 128, 1024);
+        int load = 0, seg_no = 0;   // ring loads used, runs
+        uint32_t used[2] = {0, 0};  // jobs of each S buffer whose P has been taken
+        bool ok = true;
+        // The whole warp runs the loop (its values stay uniform, as the MMA's
+        // operands have to be); one elected lane issues.
+        while (ok && tree_next<D>(a, run, pref, ent)) {
+            const int nt = __shfl_sync(0xFFFFFFFFu, run.t1 - run.t0, 0);
+            const bool two = __shfl_sync(0xFFFFFFFFu, (int)two_rows(), 0);
+            const int jobs = two ? 2 * nt : nt;
+            auto qk = [&](int j) {
+                const int b = j & 1, ld = load + 2 * (two ? j >> 1 : j), s = ld % S;
+                if (!__all_sync(0xFFFFFFFFu, tc_wait(&sh.full[s], (ld / S) & 1u, abort))) return false;
                 tc_fence_after();
-                const uint8_t *st = ring + (size_t)s * kStage;
+                const uint64_t dk = d_k + (uint32_t)s * (kStage >> 4), dq = d_q + (two && b ? kQBytes >> 4 : 0);
+                if (elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t blk = ks / 4, in = (ks % 4) * 32;
-                    tc_mma(tmem + (uint32_t)(x & 1) * 128, smem_desc_sw128(s_q + blk * kTreeM * 128 + in, 16, 1024),
-                           smem_desc_sw128(st + blk * NT * 128 + in, 16, 1024), id_qk, ks > 0);
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        tc_mma(tmem + (uint32_t)b * 128, dq + (ks / 4) * (kTreeM * 8) + (ks % 4) * 2,
+                               dk + (ks / 4) * (NT * 8) + (ks % 4) * 2, id_qk, ks > 0);
+                    tc_commit(&sh.s_full[b]);
+                    if (!two || b) tc_commit(&sh.empty[s]);
                 }
-                tc_commit(&sh.s_full[x & 1]);
-                tc_commit(&sh.empty[s]);
+                __syncwarp();
                 return true;
             };
-            while (ok && walk.next(a, NT, sg)) {
-                const int nt = sg.t1 - sg.t0;
-                ok = tc_wait(&sh.q_full, seg_no & 1u, abort);
+            ok = __all_sync(0xFFFFFFFFu, tc_wait(&sh.q_full, seg_no & 1u, abort));
+            tc_fence_after();
+            ok = ok && qk(0) && (jobs < 2 || qk(1));
+            for (int j = 0; ok && j < jobs; ++j) {
+                const int b = j & 1, ld = load + 2 * (two ? j >> 1 : j) + 1, s = ld % S;
+                ok = tc_wait(&sh.p_full[b], used[b] & 1u, abort) && tc_wait(&sh.full[s], (ld / S) & 1u, abort);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                ++used[b];
                 tc_fence_after();
-                ok = ok && qk(tau, load);
-                for (int i = 0; ok && i < nt; ++i) {
-                    if (i + 1 < nt && !qk(tau + i + 1, load + 2 * i + 2)) {
-                        ok = false;
-                        break;
-                    }
-                    const int x = tau + i, ld = load + 2 * i + 1, s = ld % S;
-                    if (!tc_wait(&sh.p_full[x & 1], (x >> 1) & 1u, abort) ||
-                        !tc_wait(&sh.full[s], (ld / S) & 1u, abort)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint8_t *st = ring + (size_t)s * kStage;
+                const uint64_t dv = d_v + (uint32_t)s * (kStage >> 4);
+                if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < NT / 16; ++ks)
-                        tc_mma_ta(tmem + kO, tmem + (uint32_t)(x & 1) * 128 + ks * 8,
-                                  smem_desc_sw128(st + ks * 2048, NT * 128, 1024), id_pv, i > 0 || ks > 0);
-                    tc_commit(&sh.pv_done);
-                    tc_commit(&sh.empty[s]);
+                        tc_mma_ta(tmem + kO + (NG == 2 ? (uint32_t)b * D : 0u), tmem + (uint32_t)b * 128 + ks * 8,
+                                  dv + ks * 128, id_pv, j >= NG || ks > 0);
+                    // the softmax waits for P V where it changes O (one group), and at the end of the run
+                    if (NG == 1 || j + 2 >= jobs) tc_commit(&sh.pv_done[NG == 2 ? b : 0]);
+                    if (!two || b) tc_commit(&sh.empty[s]);
                 }
-                load += 2 * nt;
-                tau += nt;
-                ++seg_no;
+                __syncwarp();
+                if (j + 2 < jobs) ok = qk(j + 2);
             }
+            load += 2 * nt;
+            ++seg_no;
         }
     } else {
         // ----------------------------------------------------------- softmax
-        const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-        int load = 0, tau = 0;
+        const int grp = warp >> 2, gw = warp & 3;  // gw: its tensor-memory lanes
+        const int gt = gw * 32 + lane;             // row within the group's 128
+        const uint32_t lanes = tmem + ((uint32_t)(gw * 32) << 16);
+        int load = 0;
+        uint32_t seen[2] = {0, 0}, done = 0;  // S of each buffer taken, P V waited for
         bool ok = true;
-        while (walk.next(a, NT, sg)) {
-            const int nt = sg.t1 - sg.t0, row0 = sg.rt * kTreeM, rows = min(kTreeM, sg.e.fresh * a.G - row0);
-            const int row = row0 + tid, t = row / a.G;
-            const bool live = tid < rows, warp_live = warp * 32 < rows;
+        while (tree_next<D>(a, run, pref, ent)) {
+            const int nt = run.t1 - run.t0, row0 = run.rt * tree_rows(D);
+            const bool two = two_rows(), join = NG == 2 && !two;
+            const int base = two ? grp * kTreeM : 0;  // first row of this thread's S within the item
+            const int rows = min(kTreeM, run.e.fresh * a.G - row0 - base);
+            const int row = row0 + base + gt, t = row / a.G;
+            const bool live = gt < rows, warp_live = gw * 32 < rows;
             // Q rows of this item, swizzled as TMA would: 16-byte chunk c of
-            // row r of a 64-column block goes to chunk c ^ (r mod 8)
+            // row r of a 64-column block goes to chunk c ^ (r mod 8).  The
+            // warps that work on the same rows load 16 of them each, else 32.
             if (ok) {
-                for (int x = lane; x < 32 * (D / 8); x += 32) {
-                    const int r = warp * 32 + x / (D / 8), c = x % (D / 8);
-                    if (r >= rows) continue;
-                    const int rr = row0 + r, tt = rr / a.G;
-                    const uint4 v = *reinterpret_cast<const uint4 *>(
-                        a.q + ((size_t)sg.i * a.T + tt) * a.q_stride + (size_t)(sg.g * a.G + rr - tt * a.G) * D + c * 8);
-                    *reinterpret_cast<uint4 *>(s_q + (c / 8) * kTreeM * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+                constexpr int kC = D / 8, kB = 4;  // chunks of a row; loads in flight
+                const int span = join ? 16 : 32, r0 = (join ? warp : gw) * span;
+                uint8_t *to = s_q + (two ? grp * kQBytes : 0);
+                const uint16_t *from = a.q + (size_t)run.i * a.T * a.q_stride + (size_t)run.g * a.G * D;
+                for (int k0 = 0; k0 < span * kC / 32; k0 += kB) {
+                    uint4 v[kB];
+#pragma unroll
+                    for (int k = 0; k < kB; ++k) {
+                        const int x = (k0 + k) * 32 + lane, r = r0 + x / kC, c = x % kC;
+                        const int rr = row0 + base + r, tt = rr / a.G;
+                        if (x < span * kC && r < rows)
+                            v[k] = *reinterpret_cast<const uint4 *>(from + (size_t)tt * a.q_stride +
+                                                                    (size_t)(rr - tt * a.G) * D + c * 8);
+                    }
+#pragma unroll
+                    for (int k = 0; k < kB; ++k) {
+                        const int x = (k0 + k) * 32 + lane, r = r0 + x / kC, c = x % kC;
+                        if (x < span * kC && r < rows)
+                            *reinterpret_cast<uint4 *>(to + (c / 8) * kTreeM * 128 + r * 128 +
+                                                       (((c & 7) ^ (r & 7)) << 4)) = v[k];
+                    }
                 }
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.q_full);
             }
             float m = -CUDART_INF_F, l = 0.f;  // the maximum that P and the sum refer to (of S unscaled)
-            for (int i = 0; ok && i < nt; ++i) {
-                const int x = tau + i, p0 = (sg.t0 + i) * NT;
-                const uint32_t sc = lanes + (uint32_t)(x & 1) * 128;
-                ok = tc_wait(&sh.s_full[x & 1], (x >> 1) & 1u, abort);
+            const int step = join ? 2 : 1, first = join ? grp : 0;
+            for (int i = first; i < nt; i += step) {
+                const int b = NG == 2 ? grp : i & 1, p0 = (run.t0 + i) * NT;
+                const uint32_t sc = lanes + (uint32_t)b * 128;
+                const bool tail = p0 + NT > run.e.len;  // new tokens, or nothing, in this tile
+                uint32_t bits[NT / 32];
+                if (tail) {
+#pragma unroll
+                    for (int c = 0; c < NT / 32; ++c) bits[c] = live ? tree_bits(a, run.i, t, run.e, p0 + 32 * c) : 0u;
+                }
+                ok = ok && tc_wait(&sh.s_full[b], seen[b] & 1u, abort);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
+                ++seen[b];
                 tc_fence_after();
-                float s[NT];
-                const bool tail = p0 + NT > sg.e.len;  // new tokens, or nothing, in this tile
-                if (warp_live) {
-#pragma unroll
-                    for (int c = 0; c < NT; c += 32) tmem_ld32(sc + c, s + c);
-                    tmem_wait_ld();
+                float lo[32], hi[32];  // 32 scores each
+                float top = 0.f;
+                auto hide = [&](float *v, uint32_t w) {
                     if (tail) {
 #pragma unroll
-                        for (int c = 0; c < NT; c += 32) {
-                            const uint32_t w = live ? tree_bits(a, sg.i, t, sg.e, p0 + c) : 0u;
+                        for (int k = 0; k < 32; ++k) v[k] = (w >> k) & 1u ? v[k] : -CUDART_INF_F;
+                    }
+                };
+                auto max32 = [&](const float *v) {
+                    float x[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) s[c + k] = (w >> k) & 1u ? s[c + k] : -CUDART_INF_F;
-                        }
+                    for (int k = 4; k < 32; k += 2) x[(k / 2) & 3] = max3(x[(k / 2) & 3], v[k], v[k + 1]);
+                    return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+                };
+                if (warp_live) {
+                    // the upper half of 128 scores first; the lower stays in registers
+#pragma unroll
+                    for (int c = NT - 64; c >= 0; c -= 64) {
+                        tmem_ld32(sc + c, lo);
+                        tmem_ld32(sc + c + 32, hi);
+                        tmem_wait_ld(lo);
+                        hide(lo, bits[c / 32]);
+                        top = c == NT - 64 ? max32(lo) : fmaxf(top, max32(lo));
+                        tmem_wait_ld(hi);
+                        hide(hi, bits[c / 32 + 1]);
+                        top = fmaxf(top, max32(hi));
                     }
                 }
-                if (i > 0) {
-                    ok = tc_wait(&sh.pv_done, (x - 1) & 1u, abort);
+                if (NG == 1 && i > 0) {  // P V of the last tile (two groups: S came after it)
+                    ok = tc_wait(&sh.pv_done[0], done & 1u, abort);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
+                    ++done;
                     tc_fence_after();
                 }
                 if (warp_live) {
-                    float top = s[0];
-#pragma unroll
-                    for (int c = 1; c < NT; ++c) top = fmaxf(top, s[c]);
                     const bool grew = live && (top - m) * a.scale > kGrow;  // also from -inf
                     if (__any_sync(0xFFFFFFFFu, grew)) {
                         const float f = grew ? ex2((m - top) * a.scale) : 1.f;
                         if (grew) m = top;
                         l *= f;
-                        if (i > 0) {
+                        if (i > first) {
+                            const uint32_t oc = lanes + kO + (uint32_t)(grp * D);
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 16) {
+                                float o[16];
+                                tmem_ld16n(oc + c, o);
+                                tmem_wait_ld16(o);
 #pragma unroll
-                            for (int c = 0; c < D; c += 32) {
-                                float o[32];
-                                tmem_ld32(lanes + kO + c, o);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) o[k] *= f;
-                                tmem_st32(lanes + kO + c, reinterpret_cast<const uint32_t *>(o));
+                                for (int k = 0; k < 16; ++k) o[k] *= f;
+                                tmem_st16(oc + c, reinterpret_cast<const uint32_t *>(o));
                             }
-                            tmem_wait_st();
                         }
                     }
                     const float ms = kBias - (m == -CUDART_INF_F ? 0.f : m) * a.scale;
-                    uint32_t pk[NT / 2];
-                    float sum0 = 0.f, sum1 = 0.f;
+                    const uint64_t scale2 = pair(a.scale, a.scale), ms2 = pair(ms, ms);
+                    uint64_t sum0 = 0, sum1 = 0;
+                    auto exps = [&](const float *v, uint32_t to) {
+                        uint32_t pk[16];
 #pragma unroll
-                    for (int c = 0; c < NT; c += 2) {
-                        const float e0 = ex2(fmaf(s[c], a.scale, ms)), e1 = ex2(fmaf(s[c + 1], a.scale, ms));
-                        sum0 += e0;
-                        sum1 += e1;
-                        pk[c / 2] = pack16<BF16>(e0, e1);
+                        for (int k = 0; k < 32; k += 2) {
+                            float e0, e1;
+                            unpair(fma2(pair(v[k], v[k + 1]), scale2, ms2), e0, e1);
+                            e0 = ex2(e0);
+                            e1 = ex2(e1);
+                            if (k & 2)
+                                sum1 = add2(sum1, pair(e0, e1));
+                            else
+                                sum0 = add2(sum0, pair(e0, e1));
+                            pk[k / 2] = pack16<BF16>(e0, e1);
+                        }
+                        tmem_st16(to, pk);
+                    };
+                    // P goes over S from the front: over scores in registers, or used up
+                    exps(lo, sc);
+                    if constexpr (NT == 128) tmem_ld32(sc + 64, lo);
+                    exps(hi, sc + 16);
+                    if constexpr (NT == 128) {
+                        tmem_ld32(sc + 96, hi);
+                        tmem_wait_ld(lo);
+                        hide(lo, bits[2]);
+                        exps(lo, sc + 32);
+                        tmem_wait_ld(hi);
+                        hide(hi, bits[3]);
+                        exps(hi, sc + 48);
                     }
-                    l += sum0 + sum1;
-#pragma unroll
-                    for (int c = 0; c < NT / 2; c += 32) tmem_st32(sc + c, pk + c);
+                    float x, y;
+                    unpair(add2(sum0, sum1), x, y);
+                    l += x + y;
                     tmem_wait_st();
                 }
-                if (tail) {
+                if (tail && (!two || grp == 0)) {
                     // V rows of new tokens with an infinity or NaN, and rows
-                    // behind the last token, become zeros
+                    // behind the last token, become zeros; with two row tiles
+                    // by the first group, whose P V comes first
                     const int ld = load + 2 * i + 1, st = ld % S;
                     ok = tc_wait(&sh.full[st], (ld / S) & 1u, abort);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
-                    const int pos = p0 + tid;
-                    if (tid < NT && pos >= sg.e.len) {
-                        uint8_t *vr = ring + (size_t)st * kStage + tid * 128;
-                        bool clear = pos >= sg.e.len + sg.e.fresh;
+                    const int pos = p0 + gt;
+                    if (gt < NT && pos >= run.e.len) {
+                        uint8_t *vr = ring + (size_t)st * kStage + gt * 128;
+                        auto chunk = [&](int c) {  // 16-byte chunk c of the row
+                            return reinterpret_cast<uint4 *>(vr + (c / 8) * NT * 128 + (((c & 7) ^ (gt & 7)) << 4));
+                        };
+                        bool clear = pos >= run.e.len + run.e.fresh;
                         if (!clear) {
-                            for (int c = 0; c < D / 8; ++c)
-                                clear = clear || any_nonfinite<BF16>(*reinterpret_cast<const uint4 *>(
-                                                     vr + (c / 8) * NT * 128 + (((c & 7) ^ (tid & 7)) << 4)));
+#pragma unroll 8
+                            for (int c = 0; c < D / 8; ++c) clear |= any_nonfinite<BF16>(*chunk(c));
                             if (clear) *reinterpret_cast<volatile int *>(&sh.bad_v) = 1;
                         }
                         if (clear)
-                            for (int c = 0; c < D / 8; ++c)
-                                *reinterpret_cast<uint4 *>(vr + (c / 8) * NT * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                            for (int c = 0; c < D / 8; ++c) *chunk(c) = make_uint4(0, 0, 0, 0);
                     }
                     fence_async_smem();
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_full[x & 1]);
+                if (lane == 0) mbar_arrive(&sh.p_full[b]);
             }
-            if (ok) ok = __all_sync(0xFFFFFFFFu, tc_wait(&sh.pv_done, (tau + nt - 1) & 1u, abort));
-            tc_fence_after();
-            load += 2 * nt;
-            tau += nt;
             // ------------------------------------------------------ epilogue
-            const bool whole = sg.t0 == 0 && sg.t1 == sg.tiles;
-            const bool add = ok && *reinterpret_cast<volatile int *>(&sh.bad_v) && sg.t1 * NT > sg.e.len;
+            TreeOut w;
+            w.mine = first < nt;  // this group had a tile (group 0 always has)
+            if (ok && w.mine) {
+                ok = __all_sync(0xFFFFFFFFu, tc_wait(&sh.pv_done[grp], done & 1u, abort));
+                ++done;
+            }
+            load += 2 * nt;
             const float nan = CUDART_NAN_F;
+            if (join) {
+                sh.ml[grp][gt] = ok ? make_float2(m * a.scale, l) : make_float2(nan, nan);
+                tc_fence_before();
+                softmax_sync<NG>();
+            }
+            tc_fence_after();
+            w.ok = ok;
+            w.live = live;
+            w.whole = run.t0 == 0 && run.t1 == run.tiles;
+            w.m2 = m * a.scale;
+            w.bias = kBias;
+            w.f0 = 1.f;
+            w.f1 = 0.f;
+            bool other = false;
+            if (join) {  // weights of the groups' results; each thread writes half of the row
+                const float mx = sh.ml[grp ^ 1][gt].x, lx = sh.ml[grp ^ 1][gt].y;
+                other = grp == 1 || nt > 1;
+                const float top = fmaxf(w.m2, mx), tm = top == -CUDART_INF_F ? 0.f : top;
+                w.f0 = ex2(w.m2 - tm);
+                w.f1 = ex2(mx - tm);
+                l = (w.mine ? l * w.f0 : 0.f) + (other ? lx * w.f1 : 0.f);
+                w.m2 = top;
+            }
             if (warp_live) {
-                const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-                const int h = sg.g * a.G + row - t * a.G;
-                uint16_t *to = a.out + ((size_t)sg.i * a.T + t) * a.out_stride + (size_t)h * D;
-                float *rec = a.part_o + ((size_t)sg.slot * a.rows_cap + tid) * D;
-#pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    float o[32];
-                    if (ok) {
-                        tmem_ld32(lanes + kO + c, o);
-                        tmem_wait_ld();
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = nan;
-                    }
-                    if (live) {
-                        if (add)
-                            tree_add_nonfinite<D, BF16>(a, sg, NT, row, (m == -CUDART_INF_F ? 0.f : m) * a.scale,
-                                                        kBias, c, o);
-                        if (whole) {
-#pragma unroll
-                            for (int k = 0; k < 32; k += 8) {
-                                uint4 w;
-                                w.x = pack16<BF16>(o[k] * inv, o[k + 1] * inv);
-                                w.y = pack16<BF16>(o[k + 2] * inv, o[k + 3] * inv);
-                                w.z = pack16<BF16>(o[k + 4] * inv, o[k + 5] * inv);
-                                w.w = pack16<BF16>(o[k + 6] * inv, o[k + 7] * inv);
-                                *reinterpret_cast<uint4 *>(to + c + k) = w;
-                            }
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 32; k += 4)
-                                *reinterpret_cast<float4 *>(rec + c + k) =
-                                    make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-                        }
-                    }
-                    __syncwarp();
-                }
-                if (live && !whole)
-                    a.part_ml[(size_t)sg.slot * a.rows_cap + tid] = ok ? make_float2(m * a.scale, l) : make_float2(nan, nan);
+                w.inv = w.whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+                w.row = row;
+                w.t = t;
+                w.o_mine = lanes + kO + (uint32_t)(grp * D);
+                w.o_other = other ? lanes + kO + (uint32_t)((grp ^ 1) * D) : 0u;
+                w.c0 = join ? grp * (D / 2) : 0;
+                w.c1 = join ? w.c0 + D / 2 : D;
+                w.rec = a.part_o + (size_t)run.slot * (D / 4) * a.rows_cap + base + gt;
+                w.to = a.out + ((size_t)run.i * a.T + t) * a.out_stride + (size_t)(run.g * a.G + row - t * a.G) * D;
+                if (__any_sync(0xFFFFFFFFu, *reinterpret_cast<volatile int *>(&sh.bad_v) && run.t1 * NT > run.e.len))
+                    tree_write_add<D, BF16>(a, run, w);
+                else
+                    tree_write<D, BF16, false>(a, run, w);
+                if (live && !w.whole && (!join || grp == 0))
+                    a.part_ml[(size_t)run.slot * a.rows_cap + base + gt] = ok ? make_float2(w.m2, l) : make_float2(nan, nan);
             }
             tc_fence_before();
+            if (join) softmax_sync<NG>();  // O and the maxima have been read
         }
     }
     // After a wait ran out some copies may be in flight: let the last one of
     // every stage land before the shared memory is freed.
     __syncwarp();
-    if (warp == 4 && lane == 0 && *abort) {
+    if (warp == kLoader && lane == 0 && *abort) {
         for (int x = issued > S ? issued - S : 0; x < issued; ++x)
             tc_drain(&sh.full[x % S], (uint32_t)(x / S) & 1u, kTcTimeoutNs);
         pages_fail(a.p.state, kPgTimeout, 0, blockIdx.x);
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 5) {
+    if (warp == kIssuer) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
     }
 }
 
-// Joins the records of every item that more than one CTA worked on: one warp
-// per row, CTA (x, y, z) the rows 8 x .. 8 x + 7 of row tile z of KV head
-// y of the entries in turn.
+// Joins the records of every item that more than one CTA worked on: CTA
+// (x, i, g) rows 8 x .. 8 x + 7 of KV head g of entry i, a thread 4 columns of
+// one row (the 8 rows of a column block are side by side in a record).
 constexpr int kCombineRows = 8;
+constexpr int kCombineThreads = 256;
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kCombineRows * 32) tree_combine_kernel(const TreeArgs a, int grid) {
-    constexpr int NT = tree_nt(D), E = D / 32;
-    __shared__ long long s_before, s_total;
-    __shared__ long long s_red[2 * kCombineRows];
+__global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const __grid_constant__ TreeArgs a, int grid) {
+    constexpr int NT = tree_nt(D), kRows = tree_rows(D);
+    __shared__ long long s_red[2][kCombineThreads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int per_rt = (kTreeM + kCombineRows - 1) / kCombineRows;
-    const int i = blockIdx.y, rt = blockIdx.x / per_rt, r = (blockIdx.x - rt * per_rt) * kCombineRows + warp;
-    const int g = blockIdx.z;
+    const int i = blockIdx.y, g = blockIdx.z, row = blockIdx.x * kCombineRows + (lane & 7);
     // units before entry i, and of all entries
     long long before = 0, total = 0;
-    for (int k = threadIdx.x; k < a.n; k += blockDim.x) {
+    for (int k = threadIdx.x; k < a.n; k += kCombineThreads) {
         const PagesEntry e = pages_entry(a.p, a.seqs, a.n_new, k, a.T);
-        const long long u = tree_units(a, TreeEntry{e.seq, e.len, e.fresh}, NT);
+        const long long u = tree_units<D>(a, TreeEntry{e.seq, e.len, e.fresh});
         total += u;
         if (k < i) before += u;
     }
@@ -630,81 +853,83 @@ __global__ void __launch_bounds__(kCombineRows * 32) tree_combine_kernel(const T
         total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
     }
     if (lane == 0) {
-        s_red[2 * warp] = before;
-        s_red[2 * warp + 1] = total;
+        s_red[0][warp] = before;
+        s_red[1][warp] = total;
     }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        long long b = 0, t = 0;
-        for (int k = 0; k < kCombineRows; ++k) {
-            b += s_red[2 * k];
-            t += s_red[2 * k + 1];
-        }
-        s_before = b;
-        s_total = t;
-    }
-    __syncthreads();
     const PagesEntry e = pages_entry(a.p, a.seqs, a.n_new, i, a.T);
-    const int row = rt * kTreeM + r;
+    __syncthreads();
+    before = total = 0;
+#pragma unroll
+    for (int k = 0; k < kCombineThreads / 32; ++k) {
+        before += s_red[0][k];
+        total += s_red[1][k];
+    }
     pdl_wait();  // the records are complete
     if (!e.fresh || row >= e.fresh * a.G) return;
-    const int tiles = (e.len + e.fresh + NT - 1) / NT, rts = (e.fresh * a.G + kTreeM - 1) / kTreeM;
-    const long long U = s_total, u0 = s_before + ((long long)g * rts + rt) * tiles, u1 = u0 + tiles;
+    const int rt = row / kRows, r = row - rt * kRows;
+    const int tiles = (e.len + e.fresh + NT - 1) / NT, rts = (e.fresh * a.G + kRows - 1) / kRows;
+    const long long U = total, u0 = before + ((long long)g * rts + rt) * tiles, u1 = u0 + tiles;
     const int ctas = tree_ctas(U, grid);
     // the CTA of unit u is the last one whose first unit is at most u
     const int c0 = (int)(((u0 + 1) * ctas - 1) / U), c1 = (int)((u1 * ctas - 1) / U);
     if (c0 == c1) return;
+    // of these CTAs only the first one's record can be its second
+    const int slot0 = 2 * c0 + (tree_first(U, ctas, c0) < u0 ? 1 : 0);
+    auto slot = [&](int c) { return (size_t)(c == c0 ? slot0 : 2 * c); };
     float M = -CUDART_INF_F;
-    auto slot = [&](int c) { return (size_t)(2 * c + (tree_first(U, ctas, c) < u0 ? 1 : 0)) * a.rows_cap + r; };
-    for (int c = c0; c <= c1; ++c) M = fmaxf(M, a.part_ml[slot(c)].x);
-    float o[E], L = 0.f;
-#pragma unroll
-    for (int k = 0; k < E; ++k) o[k] = 0.f;
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) M = fmaxf(M, a.part_ml[slot(c) * a.rows_cap + r].x);
     const float Ms = M == -CUDART_INF_F ? 0.f : M;
-    for (int c = c0; c <= c1; ++c) {
-        const size_t at = slot(c);
-        const float2 ml = a.part_ml[at];
-        const float f = ex2(ml.x - Ms);
-        L = fmaf(f, ml.y, L);
-#pragma unroll
-        for (int k = 0; k < E; k += 2) {
-            const float2 v = *reinterpret_cast<const float2 *>(a.part_o + at * D + k * 32 + lane * 2);
-            o[k] = fmaf(f, v.x, o[k]);
-            o[k + 1] = fmaf(f, v.y, o[k + 1]);
-        }
-    }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
     const int t = row / a.G;
     uint16_t *to = a.out + ((size_t)i * a.T + t) * a.out_stride + (size_t)(g * a.G + row - t * a.G) * D;
-#pragma unroll
-    for (int k = 0; k < E; k += 2)
-        *reinterpret_cast<uint32_t *>(to + k * 32 + lane * 2) = pack16<BF16>(o[k] * inv, o[k + 1] * inv);
+    for (int c4 = warp * 4 + (lane >> 3); c4 < D / 4; c4 += kCombineThreads / 8) {
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float L = 0.f;
+#pragma unroll 4
+        for (int c = c0; c <= c1; ++c) {
+            const float2 ml = a.part_ml[slot(c) * a.rows_cap + r];
+            const float4 v = a.part_o[(slot(c) * (D / 4) + c4) * a.rows_cap + r];
+            const float f = ex2(ml.x - Ms);
+            L = fmaf(f, ml.y, L);
+            o.x = fmaf(f, v.x, o.x);
+            o.y = fmaf(f, v.y, o.y);
+            o.z = fmaf(f, v.z, o.z);
+            o.w = fmaf(f, v.w, o.w);
+        }
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        *reinterpret_cast<uint2 *>(to + c4 * 4) =
+            make_uint2(pack16<BF16>(o.x * inv, o.y * inv), pack16<BF16>(o.z * inv, o.w * inv));
+    }
 }
 
 // ------------------------------------------------------------------ host side
-static int tree_rows(int T, int G) { return (long long)T * G < kTreeM ? T * G : kTreeM; }
+static int tree_rows_cap(int T, int G, int d) {
+    const long long rows = (long long)T * G;
+    return rows < mk::tree_rows(d) ? (int)rows : mk::tree_rows(d);
+}
 
 static size_t tree_scratch(int T, int nq, int nkv, int d, int grid) {
-    return (size_t)2 * grid * tree_rows(T, nq / nkv) * (d + 2) * sizeof(float);
+    return (size_t)2 * grid * tree_rows_cap(T, nq / nkv, d) * (d + 2) * sizeof(float);
 }
 
 template <int D, bool BF16>
 static cudaError_t launch_tree(const CUtensorMap &mk, const CUtensorMap &mv, TreeArgs &a, int grid, cudaStream_t s) {
     constexpr int stage = tree_nt(D) * D * 2;
-    const int fixed = 1024 + kTreeM * D * 2 + (int)sizeof(TreeShared) + (a.n + 1) * 8 + a.n * (int)sizeof(TreeEntry);
+    a.q_tiles = tree_groups(D) == 2 && (long long)a.T * a.G > kTreeM ? 2 : 1;
+    const int fixed = 1024 + a.q_tiles * kTreeM * D * 2 + (int)sizeof(TreeShared) + (a.n + 1) * 8 +
+                      a.n * (int)sizeof(TreeEntry);
     a.stages = (227 * 1024 - fixed) / stage;
     if (a.stages > kTreeMaxStages) a.stages = kTreeMaxStages;
     static std::atomic<unsigned long long> configured{0};
     cudaError_t e = tc_allow_smem(reinterpret_cast<const void *>(attn_tree_kernel<D, BF16>), 227 * 1024, configured);
     if (e != cudaSuccess) return e;
-    attn_tree_kernel<D, BF16><<<grid, 192, fixed + a.stages * stage, s>>>(mk, mv, a);
+    attn_tree_kernel<D, BF16><<<grid, tree_threads(D), fixed + a.stages * stage, s>>>(mk, mv, a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    const int rts = (int)(((long long)a.T * a.G + kTreeM - 1) / kTreeM);
-    const int per_rt = rts > 1 ? kTreeM / kCombineRows : (a.T * a.G + kCombineRows - 1) / kCombineRows;
-    cfg.gridDim = dim3((unsigned)(rts > 1 ? rts * per_rt : per_rt), (unsigned)a.n, (unsigned)a.p.n_kv_heads);
-    cfg.blockDim = dim3(kCombineRows * 32);
+    cfg.gridDim = dim3((unsigned)(((long long)a.T * a.G + kCombineRows - 1) / kCombineRows), (unsigned)a.n,
+                       (unsigned)a.p.n_kv_heads);
+    cfg.blockDim = dim3(kCombineThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -759,9 +984,9 @@ extern "C" mk_status mk_attention_tree(const mk_pages *p, int layer, const void 
     a.words = (T + 31) / 32;
     a.nq = n_heads;
     a.G = n_heads / p->n_kv_heads;
-    a.rows_cap = tree_rows(T, a.G);
-    a.part_o = static_cast<float *>(scratch);
-    a.part_ml = reinterpret_cast<float2 *>(a.part_o + (size_t)2 * grid * a.rows_cap * d);
+    a.rows_cap = tree_rows_cap(T, a.G, d);
+    a.part_o = static_cast<float4 *>(scratch);
+    a.part_ml = reinterpret_cast<float2 *>(a.part_o + (size_t)2 * grid * a.rows_cap * (d / 4));
     a.scale = (float)(1.4426950408889634 / std::sqrt((double)d));
     // a copy covers the part of a tile that lies in one page
     const int nt = tree_nt(d);
