@@ -8,8 +8,8 @@
 //   a mask).
 //
 // The T new tokens of the G = nq / nkv query heads that share a KV head are
-// the rows of one matrix (row r = t G + g), 128 of them the M of an MMA, so the
-// cache is read once for up to 256 rows and the arithmetic (4 d flops per row
+// the rows of one matrix (row r = t G + g), the tokens that fit 128 rows the M of
+// an MMA, so the cache is read once for up to 256 rows and the arithmetic (4 d flops per row
 // and position) stays behind the memory traffic (4 d bytes per position).  Per
 // tile of NT positions:
 //     S = Q K^T  (tensor memory, M = 128, N = NT), softmax in registers,
@@ -35,8 +35,8 @@
 // writes (o, max, sum) to scratch, at most two such records per CTA, and
 // tree_combine_kernel joins them.
 //
-// Roles: the softmax warps; one warp loads K and V tiles by TMA
-// into a ring (a page's share of a tile per copy; the lanes look up 32 pages
+// Roles: the softmax warps; one warp loads Q and, into a ring, K and V tiles by
+// TMA (a page's share of a tile per copy; the lanes look up 32 pages
 // at a time, ahead); one lane issues the MMAs: with two jobs (tile, group) in
 // flight, S of job j + 2 follows P V of job j.
 //
@@ -58,10 +58,9 @@ namespace mk {
 constexpr int kTreeM = 128;          // rows of an MMA
 constexpr int kTreeMaxStages = 12;
 
-// Softmax groups, positions of a tile and rows of an item at head size d.
+// Softmax groups and positions of a tile at head size d.
 __host__ __device__ constexpr int tree_groups(int d) { return d == 256 ? 1 : 2; }
 __host__ __device__ constexpr int tree_nt(int d) { return d == 256 ? 64 : 128; }
-__host__ __device__ constexpr int tree_rows(int d) { return kTreeM * tree_groups(d); }
 __host__ __device__ constexpr int tree_threads(int d) { return (4 * tree_groups(d) + 2) * 32; }
 
 struct TreeArgs {
@@ -75,6 +74,7 @@ struct TreeArgs {
     float2 *part_ml; // [2 x CTAs][rows_cap]: maximum (base 2, scaled), sum
     const uint16_t *k, *v;  // this layer's pages
     int n, T, words, nq, G, seg, stages, q_tiles, rows_cap;
+    int toks;        // new tokens of a row tile: 128 / G
     float scale;     // log2(e) / sqrt(d)
 };
 
@@ -95,7 +95,7 @@ struct TreeRun {
 // Shared memory behind the operand tiles.
 struct TreeShared {
     uint64_t full[kTreeMaxStages], empty[kTreeMaxStages];
-    uint64_t s_full[2], p_full[2], pv_done[2], q_full;
+    uint64_t s_full[2], p_full[2], pv_done[2], q_full, q_empty;
     TreeRun run[10];       // of each warp
     float2 ml[2][kTreeM];  // the groups' maxima (scaled) and sums at the end of a run
     uint32_t tmem;
@@ -106,7 +106,8 @@ struct TreeShared {
 template <int D>
 __device__ __forceinline__ long long tree_units(const TreeArgs &a, const TreeEntry &e) {
     if (!e.fresh) return 0;
-    const int rts = (e.fresh * a.G + tree_rows(D) - 1) / tree_rows(D), tiles = (e.len + e.fresh + tree_nt(D) - 1) / tree_nt(D);
+    const int item = tree_groups(D) * a.toks;  // new tokens of an item
+    const int rts = (e.fresh + item - 1) / item, tiles = (e.len + e.fresh + tree_nt(D) - 1) / tree_nt(D);
     return (long long)a.p.n_kv_heads * rts * tiles;
 }
 
@@ -129,7 +130,7 @@ __device__ __forceinline__ bool tree_next(const TreeArgs &a, TreeRun &r, const l
             r.i = i;
             r.e = e;
             r.tiles = (e.len + e.fresh + nt - 1) / nt;
-            const int rts = (e.fresh * a.G + tree_rows(D) - 1) / tree_rows(D);
+            const int rts = (e.fresh + tree_groups(D) * a.toks - 1) / (tree_groups(D) * a.toks);
             const long long local = r.u - pref[i];
             const int item = (int)small_div(local, r.tiles);
             r.t0 = (int)(local - (long long)item * r.tiles);
@@ -154,25 +155,29 @@ __device__ __forceinline__ int tree_ctas(long long U, int most) {
 }
 __device__ __forceinline__ long long tree_first(long long U, int ctas, int c) { return small_div(U * c, ctas); }
 
-// 32 visibility bits of row `row` (a new token) for new tokens 32 k .. 32 k + 31
+// The words of new token t's mask row: bit u of word k is new token 32 k + u
 // (k < 0: committed positions, all visible).
-__device__ __forceinline__ uint32_t tree_word(const TreeArgs &a, int i, int t, int fresh, int k) {
-    if (k < 0) return 0xFFFFFFFFu;
+__device__ __forceinline__ uint32_t tree_word(const TreeArgs &a, const uint32_t *mask_row, int t, int fresh, int k) {
     const int u0 = k * 32;
-    if (u0 >= fresh) return 0u;
     uint32_t w;
-    if (a.mask)
-        w = a.mask[((size_t)i * a.T + t) * a.words + k];
+    if (a.mask)  // loads without a branch, so that several can be in flight
+        w = mask_row[min(max(k, 0), a.words - 1)];
     else
-        w = u0 > t ? 0u : (t - u0 >= 31 ? 0xFFFFFFFFu : (2u << (t - u0)) - 1u);
-    return fresh - u0 >= 32 ? w : w & ((1u << (fresh - u0)) - 1u);
+        w = t - u0 >= 31 ? 0xFFFFFFFFu : (2u << (max(t - u0, -1) & 31)) - 1u;
+    if (!a.mask && t < u0) w = 0u;
+    const uint32_t real = fresh - u0 >= 32 ? 0xFFFFFFFFu : fresh > u0 ? (1u << (fresh - u0)) - 1u : 0u;
+    return k < 0 ? 0xFFFFFFFFu : w & real;
 }
-// ... for positions pos .. pos + 31.
-__device__ __forceinline__ uint32_t tree_bits(const TreeArgs &a, int i, int t, const TreeEntry &e, int pos) {
-    const int u = pos - e.len;
-    const int k = u >> 5, sh = u & 31;
-    const uint32_t lo = tree_word(a, i, t, e.fresh, k);
-    return sh ? __funnelshift_r(lo, tree_word(a, i, t, e.fresh, k + 1), sh) : lo;
+// Visibility of positions pos .. pos + 32 N - 1 to it.
+template <int N>
+__device__ __forceinline__ void tree_bits(const TreeArgs &a, int i, int t, const TreeEntry &e, int pos, uint32_t *bits) {
+    const int u = pos - e.len, k = u >> 5, sh = u & 31;
+    const uint32_t *row = a.mask + ((size_t)i * a.T + t) * a.words;
+    uint32_t w[N + 1];
+#pragma unroll
+    for (int x = 0; x <= N; ++x) w[x] = tree_word(a, row, t, e.fresh, k + x);
+#pragma unroll
+    for (int x = 0; x < N; ++x) bits[x] = __funnelshift_r(w[x], w[x + 1], sh);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -306,7 +311,7 @@ struct TreeOut {
     float f0, f1;              // their weights
     float inv;                 // 1 / sum for the result, 1 for a record
     float m2, bias;
-    int c0, c1, row, t;
+    int c0, c1, g, t;
     bool mine, live, whole, ok;
     float4 *rec;
     uint16_t *to;
@@ -316,7 +321,7 @@ struct TreeOut {
 // the MMA those rows of V are zeros, since 0 x inf in a row that does not see
 // the token would be NaN; here every row that does see one adds p V itself.
 template <int D, bool BF16, bool ADD>
-__device__ __forceinline__ void tree_write(const TreeArgs &a, const TreeRun &r, const TreeOut &w) {
+__device__ __forceinline__ void tree_write(const TreeArgs &a, const TreeRun &r, const TreeOut w) {
     for (int c = w.c0; c < w.c1; c += 16) {
         float o[16], x[16];
         if (w.mine && w.ok) {
@@ -333,10 +338,12 @@ __device__ __forceinline__ void tree_write(const TreeArgs &a, const TreeRun &r, 
         }
         if (w.live) {
             if constexpr (ADD) {
-                const uint16_t *q = a.q + ((size_t)r.i * a.T + w.t) * a.q_stride + (size_t)(r.g * a.G + w.row - w.t * a.G) * D;
+                const uint16_t *q = a.q + ((size_t)r.i * a.T + w.t) * a.q_stride + (size_t)(r.g * a.G + w.g) * D;
                 const int to = min(r.e.len + r.e.fresh, r.t1 * tree_nt(D));
                 for (int pos = max(r.e.len, r.t0 * tree_nt(D)); pos < to; ++pos) {
-                    if (!(tree_bits(a, r.i, w.t, r.e, pos) & 1u)) continue;
+                    uint32_t see;
+                    tree_bits<1>(a, r.i, w.t, r.e, pos, &see);
+                    if (!(see & 1u)) continue;
                     const int page = a.p.table[(size_t)r.e.seq * a.p.max_pages + pos / a.p.page_size];
                     if (page < 0 || page >= a.p.n_pages) continue;
                     const size_t at = (((size_t)page * a.p.n_kv_heads + r.g) * a.p.page_size + pos % a.p.page_size) * D;
@@ -372,14 +379,14 @@ __device__ __forceinline__ void tree_write(const TreeArgs &a, const TreeRun &r, 
     }
 }
 template <int D, bool BF16>
-__device__ __noinline__ void tree_write_add(const TreeArgs &a, const TreeRun &r, const TreeOut &w) {
+__device__ __noinline__ void tree_write_add(const TreeArgs &a, const TreeRun &r, const TreeOut w) {
     tree_write<D, BF16, true>(a, r, w);
 }
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(tree_threads(D), 1)
-    attn_tree_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                     const __grid_constant__ TreeArgs a) {
+    attn_tree_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                     const __grid_constant__ CUtensorMap map_v, const __grid_constant__ TreeArgs a) {
     constexpr int NT = tree_nt(D), NH = D / 64;  // positions of a tile, 64-column blocks of a row
     constexpr int NG = tree_groups(D), kLoader = 4 * NG, kIssuer = kLoader + 1;
     constexpr uint32_t kQBytes = kTreeM * D * 2, kStage = NT * D * 2;
@@ -407,7 +414,8 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
             mbar_init(&sh.p_full[s], 4);
             mbar_init(&sh.pv_done[s], 1);
         }
-        mbar_init(&sh.q_full, 4 * NG);
+        mbar_init(&sh.q_full, 1);
+        mbar_init(&sh.q_empty, 1);
         sh.abort = 0;
         sh.bad_v = 0;
         fence_barrier_init();
@@ -418,8 +426,8 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    if (warp == kLoader && lane < 2)
-        asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &map_v : &map_k) : "memory");
+    if (warp == kLoader && lane < 3)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &map_q : lane == 1 ? &map_k : &map_v) : "memory");
     // the listed sequences and the units before each
     for (int i = tid; i < a.n; i += blockDim.x) {
         const PagesEntry e = pages_entry(a.p, a.seqs, a.n_new, i, a.T);
@@ -465,10 +473,10 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
         run.i = lo;
         run.count = 0;
     }
-    int issued = 0;  // ring loads the loader issued
+    int issued = 0, q_issued = 0;  // the loader's ring loads and runs whose Q it loaded
     // Jobs of a run, in order: with two row tiles (both groups on every tile)
     // job j is group j & 1 of tile j / 2, else S buffer j & 1 of tile j.
-    auto two_rows = [&]() { return NG == 2 && run.e.fresh * a.G - run.rt * tree_rows(D) > kTreeM; };
+    auto two_rows = [&]() { return NG == 2 && run.e.fresh - run.rt * 2 * a.toks > a.toks; };
 
     if (warp == kLoader) {
         // ------------------------------------------------------------ loader
@@ -477,18 +485,36 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
         const int my = lane / nh, blk = lane - my * nh;
         const int nkv = a.p.n_kv_heads, ps = a.p.page_size;
         const uint32_t seg_bytes = (uint32_t)seg * D * 2, off_smem = (uint32_t)(blk * NT + my * seg) * 128u;
+        const uint32_t q_bytes = (uint32_t)(a.toks * a.G) * D * 2;
+        int slot = 0, seg_no = 0;
+        uint32_t phase = 1;  // of empty[slot]: the first round waits for nothing
         bool ok = true;
         while (ok && tree_next<D>(a, run, pref, ent)) {
             const int *row = a.p.table + (size_t)run.e.seq * a.p.max_pages;
-            const int end = run.e.len + run.e.fresh, t1 = run.t1, g = run.g;
+            const int end = run.e.len + run.e.fresh, t0 = run.t0, t1 = run.t1, g = run.g;
             const bool mine = lane < ns * nh;
             // lane x holds the page of part x % ns of tile tb + x / ns
             auto look = [&](int tb) {
                 const int t = tb + lane / ns, pos = t * NT + lane % ns * seg;
                 return t < t1 && pos < end ? row[pos / ps] : -1;
             };
-            int tb = run.t0, pages = look(tb), next = look(tb + per);
-            for (int t = tb; ok && t < t1; ++t) {
+            // Q: 64 columns x G heads x tokens are the swizzled rows of an MMA operand
+            auto load_q = [&]() {
+                if (seg_no && !tc_wait(&sh.q_empty, (seg_no - 1) & 1u, abort)) return false;
+                if (lane == 0) {
+                    const int tiles = two_rows() ? 2 : 1, tok = run.i * a.T + run.rt * NG * a.toks;
+                    mbar_arrive_expect_tx(&sh.q_full, tiles * q_bytes);
+                    for (int x = 0; x < tiles; ++x)
+                        for (int c = 0; c < NH; ++c)
+                            tma_load_4d(s_q + x * kQBytes + c * kTreeM * 128, &map_q, 0, c, g * a.G, tok + x * a.toks,
+                                        &sh.q_full);
+                }
+                ++q_issued;
+                return true;
+            };
+            int tb = t0, pages = look(tb), next = look(tb + per);
+            if (seg_no == 0) ok = load_q();
+            for (int t = t0; ok && t < t1; ++t) {
                 if (t - tb == per) {
                     tb = t;
                     pages = next;
@@ -501,23 +527,24 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
                     pages_fail(a.p.state, kPgPosition, run.i, pos);
                     page = -1;  // out of the tensor: zeros
                 }
-                const int left = (end - t * NT + seg - 1) / seg;
+                const int head = page < 0 ? -1 : page * nkv + g, left = (end - t * NT + seg - 1) / seg;
                 const uint32_t bytes = (uint32_t)(left < ns ? left : ns) * seg_bytes;
+#pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv) {
-                    const int s = issued % S;
-                    if (issued >= S) ok = tc_wait(&sh.empty[s], ((issued / S) - 1) & 1u, abort);
-                    if (!__all_sync(0xFFFFFFFFu, ok)) {
-                        ok = false;
-                        break;
-                    }
-                    if (lane == 0) mbar_arrive_expect_tx(&sh.full[s], bytes);
+                    ok = __all_sync(0xFFFFFFFFu, tc_wait(&sh.empty[slot], phase, abort));
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], bytes);
                     __syncwarp();
                     if (go)
-                        tma_load_4d(ring + (size_t)s * kStage + off_smem, kv ? &map_v : &map_k, 0, off, blk,
-                                    page < 0 ? -1 : page * nkv + g, &sh.full[s]);
+                        tma_load_4d(ring + (size_t)slot * kStage + off_smem, kv ? &map_v : &map_k, 0, off, blk, head,
+                                    &sh.full[slot]);
                     ++issued;
+                    if (++slot == S) slot = 0, phase ^= 1u;
                 }
+                // the last Q is free once its last S is done; this run's first tile does not wait for that
+                if (t == t0 && seg_no) ok = ok && __all_sync(0xFFFFFFFFu, load_q());
             }
+            ++seg_no;
         }
     } else if (warp == kIssuer) {
         // -------------------------------------------------------- MMA issuer
@@ -526,9 +553,15 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
         // 32 bytes along a row (16 rows), in units of 16 bytes
         const uint64_t d_q = smem_desc_sw128(s_q, 16, 1024), d_k = smem_desc_sw128(ring, 16, 1024),
                        d_v = smem_desc_sw128(ring, NT * 128, 1024);
-        int load = 0, seg_no = 0;   // ring loads used, runs
+        // ring slots of the next K (even loads) and the next V (odd ones)
+        int k_slot = 0, v_slot = 1, seg_no = 0;
+        uint32_t k_phase = 0, v_phase = 0;
         uint32_t used[2] = {0, 0};  // jobs of each S buffer whose P has been taken
         bool ok = true;
+        auto step = [&](int &slot, uint32_t &phase) {
+            slot += 2;
+            if (slot >= S) slot -= S, phase ^= 1u;
+        };
         // The whole warp runs the loop (its values stay uniform, as the MMA's
         // operands have to be); one elected lane issues.
         while (ok && tree_next<D>(a, run, pref, ent)) {
@@ -536,32 +569,35 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
             const bool two = __shfl_sync(0xFFFFFFFFu, (int)two_rows(), 0);
             const int jobs = two ? 2 * nt : nt;
             auto qk = [&](int j) {
-                const int b = j & 1, ld = load + 2 * (two ? j >> 1 : j), s = ld % S;
-                if (!__all_sync(0xFFFFFFFFu, tc_wait(&sh.full[s], (ld / S) & 1u, abort))) return false;
+                const int b = j & 1;
+                if (!__all_sync(0xFFFFFFFFu, tc_wait(&sh.full[k_slot], k_phase, abort))) return false;
                 tc_fence_after();
-                const uint64_t dk = d_k + (uint32_t)s * (kStage >> 4), dq = d_q + (two && b ? kQBytes >> 4 : 0);
+                const uint64_t dk = d_k + (uint32_t)k_slot * (kStage >> 4), dq = d_q + (two && b ? kQBytes >> 4 : 0);
                 if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks)
                         tc_mma(tmem + (uint32_t)b * 128, dq + (ks / 4) * (kTreeM * 8) + (ks % 4) * 2,
                                dk + (ks / 4) * (NT * 8) + (ks % 4) * 2, id_qk, ks > 0);
                     tc_commit(&sh.s_full[b]);
-                    if (!two || b) tc_commit(&sh.empty[s]);
+                    if (!two || b) tc_commit(&sh.empty[k_slot]);
+                    if (j == jobs - 1) tc_commit(&sh.q_empty);
                 }
                 __syncwarp();
+                if (!two || b) step(k_slot, k_phase);
                 return true;
             };
             ok = __all_sync(0xFFFFFFFFu, tc_wait(&sh.q_full, seg_no & 1u, abort));
             tc_fence_after();
             ok = ok && qk(0) && (jobs < 2 || qk(1));
+#pragma unroll 1
             for (int j = 0; ok && j < jobs; ++j) {
-                const int b = j & 1, ld = load + 2 * (two ? j >> 1 : j) + 1, s = ld % S;
-                ok = tc_wait(&sh.p_full[b], used[b] & 1u, abort) && tc_wait(&sh.full[s], (ld / S) & 1u, abort);
+                const int b = j & 1;
+                ok = tc_wait(&sh.full[v_slot], v_phase, abort) && tc_wait(&sh.p_full[b], used[b] & 1u, abort);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 ++used[b];
                 tc_fence_after();
-                const uint64_t dv = d_v + (uint32_t)s * (kStage >> 4);
+                const uint64_t dv = d_v + (uint32_t)v_slot * (kStage >> 4);
                 if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < NT / 16; ++ks)
@@ -569,12 +605,12 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
                                   dv + ks * 128, id_pv, j >= NG || ks > 0);
                     // the softmax waits for P V where it changes O (one group), and at the end of the run
                     if (NG == 1 || j + 2 >= jobs) tc_commit(&sh.pv_done[NG == 2 ? b : 0]);
-                    if (!two || b) tc_commit(&sh.empty[s]);
+                    if (!two || b) tc_commit(&sh.empty[v_slot]);
                 }
                 __syncwarp();
+                if (!two || b) step(v_slot, v_phase);
                 if (j + 2 < jobs) ok = qk(j + 2);
             }
-            load += 2 * nt;
             ++seg_no;
         }
     } else {
@@ -582,46 +618,16 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
         const int grp = warp >> 2, gw = warp & 3;  // gw: its tensor-memory lanes
         const int gt = gw * 32 + lane;             // row within the group's 128
         const uint32_t lanes = tmem + ((uint32_t)(gw * 32) << 16);
-        int load = 0;
+        int load = 0;  // ring loads of earlier runs
         uint32_t seen[2] = {0, 0}, done = 0;  // S of each buffer taken, P V waited for
         bool ok = true;
+        const int my_tok = gt / a.G, my_g = gt - my_tok * a.G;
         while (tree_next<D>(a, run, pref, ent)) {
-            const int nt = run.t1 - run.t0, row0 = run.rt * tree_rows(D);
+            const int nt = run.t1 - run.t0;
             const bool two = two_rows(), join = NG == 2 && !two;
-            const int base = two ? grp * kTreeM : 0;  // first row of this thread's S within the item
-            const int rows = min(kTreeM, run.e.fresh * a.G - row0 - base);
-            const int row = row0 + base + gt, t = row / a.G;
+            const int tok0 = run.rt * NG * a.toks + (two ? grp * a.toks : 0);  // first token of this row tile
+            const int rows = min(a.toks, run.e.fresh - tok0) * a.G, t = tok0 + my_tok;
             const bool live = gt < rows, warp_live = gw * 32 < rows;
-            // Q rows of this item, swizzled as TMA would: 16-byte chunk c of
-            // row r of a 64-column block goes to chunk c ^ (r mod 8).  The
-            // warps that work on the same rows load 16 of them each, else 32.
-            if (ok) {
-                constexpr int kC = D / 8, kB = 4;  // chunks of a row; loads in flight
-                const int span = join ? 16 : 32, r0 = (join ? warp : gw) * span;
-                uint8_t *to = s_q + (two ? grp * kQBytes : 0);
-                const uint16_t *from = a.q + (size_t)run.i * a.T * a.q_stride + (size_t)run.g * a.G * D;
-                for (int k0 = 0; k0 < span * kC / 32; k0 += kB) {
-                    uint4 v[kB];
-#pragma unroll
-                    for (int k = 0; k < kB; ++k) {
-                        const int x = (k0 + k) * 32 + lane, r = r0 + x / kC, c = x % kC;
-                        const int rr = row0 + base + r, tt = rr / a.G;
-                        if (x < span * kC && r < rows)
-                            v[k] = *reinterpret_cast<const uint4 *>(from + (size_t)tt * a.q_stride +
-                                                                    (size_t)(rr - tt * a.G) * D + c * 8);
-                    }
-#pragma unroll
-                    for (int k = 0; k < kB; ++k) {
-                        const int x = (k0 + k) * 32 + lane, r = r0 + x / kC, c = x % kC;
-                        if (x < span * kC && r < rows)
-                            *reinterpret_cast<uint4 *>(to + (c / 8) * kTreeM * 128 + r * 128 +
-                                                       (((c & 7) ^ (r & 7)) << 4)) = v[k];
-                    }
-                }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.q_full);
-            }
             float m = -CUDART_INF_F, l = 0.f;  // the maximum that P and the sum refer to (of S unscaled)
             const int step = join ? 2 : 1, first = join ? grp : 0;
             for (int i = first; i < nt; i += step) {
@@ -630,8 +636,9 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
                 const bool tail = p0 + NT > run.e.len;  // new tokens, or nothing, in this tile
                 uint32_t bits[NT / 32];
                 if (tail) {
+                    tree_bits<NT / 32>(a, run.i, live ? t : 0, run.e, p0, bits);
 #pragma unroll
-                    for (int c = 0; c < NT / 32; ++c) bits[c] = live ? tree_bits(a, run.i, t, run.e, p0 + 32 * c) : 0u;
+                    for (int c = 0; c < NT / 32; ++c) bits[c] = live ? bits[c] : 0u;
                 }
                 ok = ok && tc_wait(&sh.s_full[b], seen[b] & 1u, abort);
                 ok = __all_sync(0xFFFFFFFFu, ok);
@@ -641,7 +648,7 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
                 float lo[32], hi[32];  // 32 scores each
                 float top = 0.f;
                 auto hide = [&](float *v, uint32_t w) {
-                    if (tail) {
+                    if (tail && __any_sync(0xFFFFFFFFu, w != 0xFFFFFFFFu)) {
 #pragma unroll
                         for (int k = 0; k < 32; ++k) v[k] = (w >> k) & 1u ? v[k] : -CUDART_INF_F;
                     }
@@ -792,20 +799,20 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
             }
             if (warp_live) {
                 w.inv = w.whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-                w.row = row;
+                w.g = my_g;
                 w.t = t;
                 w.o_mine = lanes + kO + (uint32_t)(grp * D);
                 w.o_other = other ? lanes + kO + (uint32_t)((grp ^ 1) * D) : 0u;
                 w.c0 = join ? grp * (D / 2) : 0;
                 w.c1 = join ? w.c0 + D / 2 : D;
-                w.rec = a.part_o + (size_t)run.slot * (D / 4) * a.rows_cap + base + gt;
-                w.to = a.out + ((size_t)run.i * a.T + t) * a.out_stride + (size_t)(run.g * a.G + row - t * a.G) * D;
+                w.rec = a.part_o + (size_t)run.slot * (D / 4) * a.rows_cap + (two ? grp * kTreeM : 0) + gt;
+                w.to = a.out + ((size_t)run.i * a.T + t) * a.out_stride + (size_t)(run.g * a.G + my_g) * D;
                 if (__any_sync(0xFFFFFFFFu, *reinterpret_cast<volatile int *>(&sh.bad_v) && run.t1 * NT > run.e.len))
                     tree_write_add<D, BF16>(a, run, w);
                 else
                     tree_write<D, BF16, false>(a, run, w);
                 if (live && !w.whole && (!join || grp == 0))
-                    a.part_ml[(size_t)run.slot * a.rows_cap + base + gt] = ok ? make_float2(w.m2, l) : make_float2(nan, nan);
+                    a.part_ml[(size_t)run.slot * a.rows_cap + (two ? grp * kTreeM : 0) + gt] = ok ? make_float2(w.m2, l) : make_float2(nan, nan);
             }
             tc_fence_before();
             if (join) softmax_sync<NG>();  // O and the maxima have been read
@@ -817,6 +824,7 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
     if (warp == kLoader && lane == 0 && *abort) {
         for (int x = issued > S ? issued - S : 0; x < issued; ++x)
             tc_drain(&sh.full[x % S], (uint32_t)(x / S) & 1u, kTcTimeoutNs);
+        if (q_issued) tc_drain(&sh.q_full, (uint32_t)(q_issued - 1) & 1u, kTcTimeoutNs);
         pages_fail(a.p.state, kPgTimeout, 0, blockIdx.x);
     }
     tc_fence_before();
@@ -828,17 +836,19 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
 }
 
 // Joins the records of every item that more than one CTA worked on: CTA
-// (x, i, g) rows 8 x .. 8 x + 7 of KV head g of entry i, a thread 4 columns of
+// (x, i, g) 8 rows of an item of KV head g of entry i, a thread 4 columns of
 // one row (the 8 rows of a column block are side by side in a record).
 constexpr int kCombineRows = 8;
 constexpr int kCombineThreads = 256;
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const __grid_constant__ TreeArgs a, int grid) {
-    constexpr int NT = tree_nt(D), kRows = tree_rows(D);
+    constexpr int NT = tree_nt(D), NG = tree_groups(D);
     __shared__ long long s_red[2][kCombineThreads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int i = blockIdx.y, g = blockIdx.z, row = blockIdx.x * kCombineRows + (lane & 7);
+    const int i = blockIdx.y, g = blockIdx.z, blocks = (a.rows_cap + kCombineRows - 1) / kCombineRows;
+    const int rt = blockIdx.x / blocks, r = (blockIdx.x - rt * blocks) * kCombineRows + (lane & 7);
+    const int gt = r & (kTreeM - 1), t = (rt * NG + r / kTreeM) * a.toks + gt / a.G;
     // units before entry i, and of all entries
     long long before = 0, total = 0;
     for (int k = threadIdx.x; k < a.n; k += kCombineThreads) {
@@ -865,9 +875,8 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const __g
         total += s_red[1][k];
     }
     pdl_wait();  // the records are complete
-    if (!e.fresh || row >= e.fresh * a.G) return;
-    const int rt = row / kRows, r = row - rt * kRows;
-    const int tiles = (e.len + e.fresh + NT - 1) / NT, rts = (e.fresh * a.G + kRows - 1) / kRows;
+    if (r >= a.rows_cap || gt >= a.toks * a.G || t >= e.fresh) return;
+    const int tiles = (e.len + e.fresh + NT - 1) / NT, rts = (e.fresh + NG * a.toks - 1) / (NG * a.toks);
     const long long U = total, u0 = before + ((long long)g * rts + rt) * tiles, u1 = u0 + tiles;
     const int ctas = tree_ctas(U, grid);
     // the CTA of unit u is the last one whose first unit is at most u
@@ -880,8 +889,7 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const __g
 #pragma unroll 4
     for (int c = c0; c <= c1; ++c) M = fmaxf(M, a.part_ml[slot(c) * a.rows_cap + r].x);
     const float Ms = M == -CUDART_INF_F ? 0.f : M;
-    const int t = row / a.G;
-    uint16_t *to = a.out + ((size_t)i * a.T + t) * a.out_stride + (size_t)(g * a.G + row - t * a.G) * D;
+    uint16_t *to = a.out + ((size_t)i * a.T + t) * a.out_stride + (size_t)(g * a.G + gt % a.G) * D;
     for (int c4 = warp * 4 + (lane >> 3); c4 < D / 4; c4 += kCombineThreads / 8) {
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         float L = 0.f;
@@ -903,9 +911,10 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const __g
 }
 
 // ------------------------------------------------------------------ host side
+// Rows of a record: those of all new tokens, or of two whole row tiles.
 static int tree_rows_cap(int T, int G, int d) {
-    const long long rows = (long long)T * G;
-    return rows < mk::tree_rows(d) ? (int)rows : mk::tree_rows(d);
+    const int toks = kTreeM / G;
+    return T <= toks ? T * G : tree_groups(d) * kTreeM;
 }
 
 static size_t tree_scratch(int T, int nq, int nkv, int d, int grid) {
@@ -913,9 +922,10 @@ static size_t tree_scratch(int T, int nq, int nkv, int d, int grid) {
 }
 
 template <int D, bool BF16>
-static cudaError_t launch_tree(const CUtensorMap &mk, const CUtensorMap &mv, TreeArgs &a, int grid, cudaStream_t s) {
+static cudaError_t launch_tree(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, TreeArgs &a,
+                               int grid, cudaStream_t s) {
     constexpr int stage = tree_nt(D) * D * 2;
-    a.q_tiles = tree_groups(D) == 2 && (long long)a.T * a.G > kTreeM ? 2 : 1;
+    a.q_tiles = tree_groups(D) == 2 && a.T > a.toks ? 2 : 1;
     const int fixed = 1024 + a.q_tiles * kTreeM * D * 2 + (int)sizeof(TreeShared) + (a.n + 1) * 8 +
                       a.n * (int)sizeof(TreeEntry);
     a.stages = (227 * 1024 - fixed) / stage;
@@ -923,12 +933,12 @@ static cudaError_t launch_tree(const CUtensorMap &mk, const CUtensorMap &mv, Tre
     static std::atomic<unsigned long long> configured{0};
     cudaError_t e = tc_allow_smem(reinterpret_cast<const void *>(attn_tree_kernel<D, BF16>), 227 * 1024, configured);
     if (e != cudaSuccess) return e;
-    attn_tree_kernel<D, BF16><<<grid, tree_threads(D), fixed + a.stages * stage, s>>>(mk, mv, a);
+    attn_tree_kernel<D, BF16><<<grid, tree_threads(D), fixed + a.stages * stage, s>>>(mq, mk, mv, a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(((long long)a.T * a.G + kCombineRows - 1) / kCombineRows), (unsigned)a.n,
-                       (unsigned)a.p.n_kv_heads);
+    const int item = tree_groups(D) * a.toks, blocks = (a.rows_cap + kCombineRows - 1) / kCombineRows;
+    cfg.gridDim = dim3((unsigned)((a.T + item - 1) / item * blocks), (unsigned)a.n, (unsigned)a.p.n_kv_heads);
     cfg.blockDim = dim3(kCombineThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -944,7 +954,9 @@ static cudaError_t launch_tree(const CUtensorMap &mk, const CUtensorMap &mv, Tre
 using namespace mk;
 
 extern "C" size_t mk_attention_tree_scratch_bytes(int T, int n_heads, int n_kv_heads, int head_dim) {
-    if (T < 1 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads || head_dim < 1) return 0;
+    if (T < 1 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads || n_heads / n_kv_heads > kTreeM ||
+        head_dim < 1)
+        return 0;
     return tree_scratch(T, n_heads, n_kv_heads, head_dim, pages_sms());
 }
 
@@ -958,6 +970,8 @@ extern "C" mk_status mk_attention_tree(const mk_pages *p, int layer, const void 
     if (n < 0 || n > kPagesMaxSeqs || T < 1 || n_heads < 1 || n_heads % p->n_kv_heads ||
         (long long)T * (n_heads / p->n_kv_heads) > (1 << 24) || (long long)n * T > (1 << 30))
         return pages_refuse(who, "bad sizes: 0 <= n <= 1024, T >= 1, n_heads a multiple of n_kv_heads");
+    if (n_heads / p->n_kv_heads > kTreeM)
+        return pages_refuse(who, "at most 128 query heads per KV head", MK_ERR_UNSUPPORTED);
     if (n == 0) return MK_OK;
     if (!q || !out || !seqs || !scratch) return pages_refuse(who, "null pointer");
     if (((uintptr_t)q | (uintptr_t)out | (uintptr_t)scratch) & 15)
@@ -984,6 +998,7 @@ extern "C" mk_status mk_attention_tree(const mk_pages *p, int layer, const void 
     a.words = (T + 31) / 32;
     a.nq = n_heads;
     a.G = n_heads / p->n_kv_heads;
+    a.toks = kTreeM / a.G;
     a.rows_cap = tree_rows_cap(T, a.G, d);
     a.part_o = static_cast<float4 *>(scratch);
     a.part_ml = reinterpret_cast<float2 *>(a.part_o + (size_t)2 * grid * a.rows_cap * (d / 4));
@@ -994,10 +1009,12 @@ extern "C" mk_status mk_attention_tree(const mk_pages *p, int layer, const void 
     if (p->max_pages > 1)
         while (p->page_size % seg) seg /= 2;
     a.seg = seg;
-    CUtensorMap mk, mv;
+    CUtensorMap mq, mk, mv;
     const uint64_t rows = (uint64_t)p->n_pages * p->n_kv_heads;
     const uint32_t blocks = seg == nt ? (uint32_t)(d / 64) : 1u;
-    if (!tc_make_map_pages(&mk, a.k, rows, (uint32_t)p->page_size, (uint32_t)d, (uint32_t)seg, blocks) ||
+    if (!tc_make_map_heads(&mq, q, (uint64_t)n * T, (uint64_t)q_stride, (uint32_t)n_heads, (uint32_t)d, (uint32_t)a.G,
+                           (uint32_t)a.toks) ||
+        !tc_make_map_pages(&mk, a.k, rows, (uint32_t)p->page_size, (uint32_t)d, (uint32_t)seg, blocks) ||
         !tc_make_map_pages(&mv, a.v, rows, (uint32_t)p->page_size, (uint32_t)d, (uint32_t)seg, blocks)) {
         pages_refuse(who, "the driver refused the tensor map");
         return MK_ERR_CUDA;
@@ -1005,10 +1022,11 @@ extern "C" mk_status mk_attention_tree(const mk_pages *p, int layer, const void 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool bf16 = p->dtype == MK_BF16;
     cudaError_t e;
-    switch (d) {
-        case 64: e = bf16 ? launch_tree<64, true>(mk, mv, a, grid, s) : launch_tree<64, false>(mk, mv, a, grid, s); break;
-        case 128: e = bf16 ? launch_tree<128, true>(mk, mv, a, grid, s) : launch_tree<128, false>(mk, mv, a, grid, s); break;
-        default: e = bf16 ? launch_tree<256, true>(mk, mv, a, grid, s) : launch_tree<256, false>(mk, mv, a, grid, s);
-    }
+    if (d == 64)
+        e = bf16 ? launch_tree<64, true>(mq, mk, mv, a, grid, s) : launch_tree<64, false>(mq, mk, mv, a, grid, s);
+    else if (d == 128)
+        e = bf16 ? launch_tree<128, true>(mq, mk, mv, a, grid, s) : launch_tree<128, false>(mq, mk, mv, a, grid, s);
+    else
+        e = bf16 ? launch_tree<256, true>(mq, mk, mv, a, grid, s) : launch_tree<256, false>(mq, mk, mv, a, grid, s);
     return pages_launched(e, who);
 }

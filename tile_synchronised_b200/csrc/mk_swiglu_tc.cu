@@ -381,6 +381,19 @@ bool tc_make_map_pages(CUtensorMap *m, const void *base, uint64_t rows, uint32_t
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool tc_make_map_heads(CUtensorMap *m, const void *base, uint64_t tokens, uint64_t stride, uint32_t heads, uint32_t d,
+                       uint32_t box_heads, uint32_t box_tokens) {
+    EncodeTiled enc = encode_fn();
+    if (!enc || d % 64) return false;
+    const cuuint64_t dims[4] = {64, d / 64, heads, tokens};
+    const cuuint64_t strides[3] = {128, (cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[4] = {64, 1, box_heads, box_tokens};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool swiglu_tc_supported(int B, int K, int N) {
     return B >= 1 && B <= 128 && K % (kTcBK * kTcSplit) == 0 && N % kTcM == 0;
 }

@@ -156,5 +156,11 @@ bool tc_make_map_packed(CUtensorMap *m, const void *base, uint64_t tiles, uint32
 // swizzled: `blocks` K-major operand blocks of 64 columns, one behind the other.
 bool tc_make_map_pages(CUtensorMap *m, const void *base, uint64_t rows, uint32_t page_size, uint32_t d,
                        uint32_t positions, uint32_t blocks);
+// Rows of heads, [tokens][heads][d] 2-byte elements with `stride` elements
+// between tokens, as a 4-D tensor (64 columns, d / 64, heads, tokens) with a
+// box of 64 columns of box_heads heads of box_tokens tokens: box_heads *
+// box_tokens rows of 128 bytes, 128-byte swizzled.
+bool tc_make_map_heads(CUtensorMap *m, const void *base, uint64_t tokens, uint64_t stride, uint32_t heads, uint32_t d,
+                       uint32_t box_heads, uint32_t box_tokens);
 
 }  // namespace mk
