@@ -57,6 +57,7 @@ namespace mk {
 
 constexpr int kTreeM = 128;          // rows of an MMA
 constexpr int kTreeMaxStages = 12;
+constexpr int kTreeMaxCtas = 256;    // of the grid, and so records of an item
 
 // Softmax groups and positions of a tile at head size d.
 __host__ __device__ constexpr int tree_groups(int d) { return d == 256 ? 1 : 2; }
@@ -147,12 +148,9 @@ __device__ __forceinline__ bool tree_next(const TreeArgs &a, TreeRun &r, const l
     return r.more;
 }
 
-// The CTAs that share U units out of `most`: at least kTreeMinUnits each.
-constexpr int kTreeMinUnits = 2;
-__device__ __forceinline__ int tree_ctas(long long U, int most) {
-    const long long want = (U + kTreeMinUnits - 1) / kTreeMinUnits;
-    return want < most ? (int)(want > 0 ? want : 1) : most;
-}
+// The CTAs that share U units out of `most`: one unit each is enough (with at
+// least 2, 4 or 8 a tree behind 1k positions took 1.2, 4 and 8 us more).
+__device__ __forceinline__ int tree_ctas(long long U, int most) { return U < most ? (int)(U > 0 ? U : 1) : most; }
 __device__ __forceinline__ long long tree_first(long long U, int ctas, int c) { return small_div(U * c, ctas); }
 
 // The words of new token t's mask row: bit u of word k is new token 32 k + u
@@ -307,12 +305,12 @@ __device__ __forceinline__ void softmax_sync() {
 
 // What a thread writes at the end of a run: columns c0 .. c1 - 1 of its row.
 struct TreeOut {
-    uint32_t o_mine, o_other;  // tensor memory of the group's O and of the other's (0: not read)
+    uint32_t o_mine, o_other;  // tensor memory of the group's O and of the other's
     float f0, f1;              // their weights
     float inv;                 // 1 / sum for the result, 1 for a record
     float m2, bias;
     int c0, c1, g, t;
-    bool mine, live, whole, ok;
+    bool mine, other, live, whole, ok;
     float4 *rec;
     uint16_t *to;
 };
@@ -322,19 +320,18 @@ struct TreeOut {
 // the token would be NaN; here every row that does see one adds p V itself.
 template <int D, bool BF16, bool ADD>
 __device__ __forceinline__ void tree_write(const TreeArgs &a, const TreeRun &r, const TreeOut w) {
+#pragma unroll 1
     for (int c = w.c0; c < w.c1; c += 16) {
         float o[16], x[16];
-        if (w.mine && w.ok) {
-            tmem_ld16n(w.o_mine + c, o);
-            tmem_wait_ld16(o);
-        }
+        tmem_ld16n(w.o_mine + c, o);
+        tmem_ld16n(w.o_other + c, x);
+        tmem_wait_ld16(o);
+        tmem_wait_ld16(x);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) o[k] = !w.ok ? CUDART_NAN_F : w.mine ? o[k] * w.f0 : 0.f;
-        if (w.o_other && w.ok) {
-            tmem_ld16n(w.o_other + c, x);
-            tmem_wait_ld16(x);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = fmaf(x[k], w.f1, o[k]);
+        for (int k = 0; k < 16; ++k) {  // an O that no tile went into is not used
+            o[k] = w.mine ? o[k] * w.f0 : 0.f;
+            o[k] = w.other ? fmaf(x[k], w.f1, o[k]) : o[k];
+            o[k] = w.ok ? o[k] : CUDART_NAN_F;
         }
         if (w.live) {
             if constexpr (ADD) {
@@ -802,7 +799,8 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
                 w.g = my_g;
                 w.t = t;
                 w.o_mine = lanes + kO + (uint32_t)(grp * D);
-                w.o_other = other ? lanes + kO + (uint32_t)((grp ^ 1) * D) : 0u;
+                w.other = other;
+                w.o_other = join ? lanes + kO + (uint32_t)((grp ^ 1) * D) : w.o_mine;
                 w.c0 = join ? grp * (D / 2) : 0;
                 w.c1 = join ? w.c0 + D / 2 : D;
                 w.rec = a.part_o + (size_t)run.slot * (D / 4) * a.rows_cap + (two ? grp * kTreeM : 0) + gt;
@@ -845,10 +843,11 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const __grid_constant__ TreeArgs a, int grid) {
     constexpr int NT = tree_nt(D), NG = tree_groups(D);
     __shared__ long long s_red[2][kCombineThreads / 32];
+    __shared__ float s_w[kTreeMaxCtas][kCombineRows];  // weight of each record's row
+    __shared__ float s_inv[kCombineRows];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int i = blockIdx.y, g = blockIdx.z, blocks = (a.rows_cap + kCombineRows - 1) / kCombineRows;
-    const int rt = blockIdx.x / blocks, r = (blockIdx.x - rt * blocks) * kCombineRows + (lane & 7);
-    const int gt = r & (kTreeM - 1), t = (rt * NG + r / kTreeM) * a.toks + gt / a.G;
+    const int rt = blockIdx.x / blocks, r0 = (blockIdx.x - rt * blocks) * kCombineRows;
     // units before entry i, and of all entries
     long long before = 0, total = 0;
     for (int k = threadIdx.x; k < a.n; k += kCombineThreads) {
@@ -874,37 +873,54 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const __g
         before += s_red[0][k];
         total += s_red[1][k];
     }
-    pdl_wait();  // the records are complete
-    if (r >= a.rows_cap || gt >= a.toks * a.G || t >= e.fresh) return;
     const int tiles = (e.len + e.fresh + NT - 1) / NT, rts = (e.fresh + NG * a.toks - 1) / (NG * a.toks);
-    const long long U = total, u0 = before + ((long long)g * rts + rt) * tiles, u1 = u0 + tiles;
-    const int ctas = tree_ctas(U, grid);
-    // the CTA of unit u is the last one whose first unit is at most u
-    const int c0 = (int)(((u0 + 1) * ctas - 1) / U), c1 = (int)((u1 * ctas - 1) / U);
-    if (c0 == c1) return;
-    // of these CTAs only the first one's record can be its second
-    const int slot0 = 2 * c0 + (tree_first(U, ctas, c0) < u0 ? 1 : 0);
-    auto slot = [&](int c) { return (size_t)(c == c0 ? slot0 : 2 * c); };
-    float M = -CUDART_INF_F;
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) M = fmaxf(M, a.part_ml[slot(c) * a.rows_cap + r].x);
-    const float Ms = M == -CUDART_INF_F ? 0.f : M;
+    int c0 = 0, c1 = 0, slot0 = 0;
+    if (rt < rts) {
+        const long long u0 = before + ((long long)g * rts + rt) * tiles, u1 = u0 + tiles;
+        const int ctas = tree_ctas(total, grid);
+        // the CTA of unit u is the last one whose first unit is at most u
+        c0 = (int)(((u0 + 1) * ctas - 1) / total);
+        c1 = (int)((u1 * ctas - 1) / total);
+        // of these CTAs only the first one's record can be its second
+        slot0 = 2 * c0 + (tree_first(total, ctas, c0) < u0 ? 1 : 0);
+    }
+    const int count = c1 - c0 + 1;
+    pdl_wait();              // the records are complete
+    if (c0 == c1) return;    // none, or the item's only CTA wrote the result
+    auto slot = [&](int c) { return (size_t)(c == 0 ? slot0 : 2 * (c0 + c)); };
+    // warp = row: its maximum, the weights and the sum
+    if (r0 + warp < a.rows_cap) {
+        float M = -CUDART_INF_F, L = 0.f;
+        for (int c = lane; c < count; c += 32) M = fmaxf(M, a.part_ml[slot(c) * a.rows_cap + r0 + warp].x);
+        M = warp_max(M);
+        if (M == -CUDART_INF_F) M = 0.f;
+        for (int c = lane; c < count; c += 32) {
+            const float2 ml = a.part_ml[slot(c) * a.rows_cap + r0 + warp];
+            const float f = ex2(ml.x - M);
+            s_w[c][warp] = f;
+            L = fmaf(f, ml.y, L);
+        }
+        L = warp_sum(L);
+        if (lane == 0) s_inv[warp] = L == 0.f ? 0.f : 1.f / L;
+    }
+    __syncthreads();
+    const int r = r0 + (lane & 7), gt = r & (kTreeM - 1), t = (rt * NG + r / kTreeM) * a.toks + gt / a.G;
+    if (r >= a.rows_cap || gt >= a.toks * a.G || t >= e.fresh) return;
+    const float inv = s_inv[lane & 7];
     uint16_t *to = a.out + ((size_t)i * a.T + t) * a.out_stride + (size_t)(g * a.G + gt % a.G) * D;
     for (int c4 = warp * 4 + (lane >> 3); c4 < D / 4; c4 += kCombineThreads / 8) {
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float L = 0.f;
-#pragma unroll 4
-        for (int c = c0; c <= c1; ++c) {
-            const float2 ml = a.part_ml[slot(c) * a.rows_cap + r];
-            const float4 v = a.part_o[(slot(c) * (D / 4) + c4) * a.rows_cap + r];
-            const float f = ex2(ml.x - Ms);
-            L = fmaf(f, ml.y, L);
+        const float4 *rec = a.part_o + (size_t)c4 * a.rows_cap + r;
+        const size_t pitch = (size_t)(D / 4) * a.rows_cap;
+#pragma unroll 8
+        for (int c = 0; c < count; ++c) {
+            const float4 v = rec[slot(c) * pitch];
+            const float f = s_w[c][lane & 7];
             o.x = fmaf(f, v.x, o.x);
             o.y = fmaf(f, v.y, o.y);
             o.z = fmaf(f, v.z, o.z);
             o.w = fmaf(f, v.w, o.w);
         }
-        const float inv = L == 0.f ? 0.f : 1.f / L;
         *reinterpret_cast<uint2 *>(to + c4 * 4) =
             make_uint2(pack16<BF16>(o.x * inv, o.y * inv), pack16<BF16>(o.z * inv, o.w * inv));
     }
@@ -915,6 +931,11 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const __g
 static int tree_rows_cap(int T, int G, int d) {
     const int toks = kTreeM / G;
     return T <= toks ? T * G : tree_groups(d) * kTreeM;
+}
+
+static int tree_grid() {
+    const int sms = pages_sms();
+    return sms < kTreeMaxCtas ? sms : kTreeMaxCtas;
 }
 
 static size_t tree_scratch(int T, int nq, int nkv, int d, int grid) {
@@ -957,7 +978,7 @@ extern "C" size_t mk_attention_tree_scratch_bytes(int T, int n_heads, int n_kv_h
     if (T < 1 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads || n_heads / n_kv_heads > kTreeM ||
         head_dim < 1)
         return 0;
-    return tree_scratch(T, n_heads, n_kv_heads, head_dim, pages_sms());
+    return tree_scratch(T, n_heads, n_kv_heads, head_dim, tree_grid());
 }
 
 extern "C" mk_status mk_attention_tree(const mk_pages *p, int layer, const void *q, long long q_stride, int n, int T,
@@ -979,7 +1000,7 @@ extern "C" mk_status mk_attention_tree(const mk_pages *p, int layer, const void 
     const int d = p->head_dim;
     if (q_stride < (long long)n_heads * d || q_stride % 8 || out_stride < (long long)n_heads * d || out_stride % 8)
         return pages_refuse(who, "a stride is shorter than a row or not a multiple of 8");
-    const int grid = pages_sms();
+    const int grid = tree_grid();
     if (scratch_bytes < tree_scratch(T, n_heads, p->n_kv_heads, d, grid))
         return pages_refuse(who, "scratch is smaller than mk_attention_tree_scratch_bytes");
     TreeArgs a{};

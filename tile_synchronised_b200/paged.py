@@ -24,30 +24,28 @@ from ._lib import MK_BF16, MK_FP16, MK_FP32, MkPages, check, load
 _TYPES = {torch.bfloat16: MK_BF16, torch.float16: MK_FP16, torch.float32: MK_FP32}
 
 
-class _On:
-    """The device and stream of one call: `stream`, or the device's current
-    one; allocations made inside belong to that stream."""
+_raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream().cuda_stream without its 2 us
 
-    def __init__(self, device: torch.device, stream):
-        self.stream = torch.cuda.current_stream(device) if stream is None else stream
-        same = stream is None and torch.cuda.current_device() == device.index
-        self.guard = None if same else torch.cuda.stream(self.stream)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.stream.cuda_stream
+def _elsewhere(device: torch.device, stream) -> bool:
+    """Does a call have to switch to another device or stream first?"""
+    if stream is None:
+        return torch.cuda.current_device() != device.index
+    if stream.device != device:
+        raise ValueError(f"the stream must be one of {device}")
+    return True
 
-    def __exit__(self, *a):
-        if self.guard is not None:
-            self.guard.__exit__(*a)
+
+def _on(device: torch.device, stream):
+    """The context of such a call: allocations made inside belong to its stream."""
+    return torch.cuda.stream(torch.cuda.current_stream(device) if stream is None else stream)
 
 
 def _ints(t, name: str, shape: tuple, device: torch.device):
     """The address of an int32 list of that shape (None stays None)."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.device != device or t.shape != shape or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {device}")
     return t.data_ptr()
 
@@ -107,41 +105,51 @@ class PagedCache:
                                self.max_seqs, self.max_pages, _TYPES[kv.dtype], kv.data_ptr(), table.data_ptr(),
                                lengths.data_ptr(), refs.data_ptr(), self._state.data_ptr())
         self._ref = C.byref(self._struct)
+        self._scratch = {}
 
     # ---------------------------------------------------------------- calls
+    def _call(self, name: str, stream, *args) -> None:
+        if _elsewhere(self.device, stream):
+            with _on(self.device, stream):
+                return self._call(name, None, *args)
+        st = getattr(self.lib, name)(self._ref, *args, _raw_stream(self.device.index))
+        if st:
+            check(st, None, name, op=True)
+
+    def _scratch_bytes(self, T: int, n_heads: int) -> int:
+        """Scratch of attention_tree, a function of these sizes alone."""
+        need = self._scratch.get((T, n_heads))
+        if need is None:
+            need = self.lib.mk_attention_tree_scratch_bytes(T, n_heads, self.n_kv_heads, self.head_dim)
+            self._scratch[T, n_heads] = need
+        return need
+
+    def _list(self, name: str, t: torch.Tensor, n: int) -> int:
+        return _ints(t, name, (n,), self.device)
+
     def reserve(self, seqs: torch.Tensor, counts: torch.Tensor, stream=None) -> None:
         """Room for counts[i] new tokens of sequence seqs[i], in pages it holds alone."""
         n = seqs.numel()
-        with _On(self.device, stream) as s:
-            check(self.lib.mk_pages_reserve(self._ref, _ints(seqs, "seqs", (n,), self.device),
-                                            _ints(counts, "counts", (n,), self.device), n, s),
-                  None, "mk_pages_reserve", op=True)
+        self._call("mk_pages_reserve", stream, self._list("seqs", seqs, n), self._list("counts", counts, n), n)
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
         """Empty sequence dst[i] shares the pages of src[i]'s committed positions."""
         n = src.numel()
-        with _On(self.device, stream) as s:
-            check(self.lib.mk_pages_fork(self._ref, _ints(src, "src", (n,), self.device),
-                                         _ints(dst, "dst", (n,), self.device), n, s), None, "mk_pages_fork", op=True)
+        self._call("mk_pages_fork", stream, self._list("src", src, n), self._list("dst", dst, n), n)
 
     def compact(self, seqs: torch.Tensor, n_keep: torch.Tensor, keep: torch.Tensor | None = None, stream=None) -> None:
         """Commit n_keep[i] new tokens of sequence seqs[i]: those at the
         ascending indexes keep[i], or the first ones."""
         n = seqs.numel()
         width = 0 if keep is None else keep.shape[-1]
-        with _On(self.device, stream) as s:
-            check(self.lib.mk_pages_compact(self._ref, _ints(seqs, "seqs", (n,), self.device),
-                                            _ints(n_keep, "n_keep", (n,), self.device),
-                                            _ints(keep, "keep", (n, width), self.device), width, n, s),
-                  None, "mk_pages_compact", op=True)
+        self._call("mk_pages_compact", stream, self._list("seqs", seqs, n), self._list("n_keep", n_keep, n),
+                   _ints(keep, "keep", (n, width), self.device), width, n)
 
     def free(self, seqs: torch.Tensor, lengths: torch.Tensor | None = None, stream=None) -> None:
         """Cut sequence seqs[i] to lengths[i] positions (0 by default) and give up the pages behind."""
         n = seqs.numel()
-        with _On(self.device, stream) as s:
-            check(self.lib.mk_pages_free(self._ref, _ints(seqs, "seqs", (n,), self.device),
-                                         _ints(lengths, "lengths", (n,), self.device), n, s),
-                  None, "mk_pages_free", op=True)
+        self._call("mk_pages_free", stream, self._list("seqs", seqs, n),
+                   None if lengths is None else self._list("lengths", lengths, n), n)
 
     def copy(self, src_pages: torch.Tensor, dst_pages: torch.Tensor, source: "PagedCache | None" = None,
              stream=None) -> None:
@@ -150,16 +158,13 @@ class PagedCache:
         src = self if source is None else source
         if src.device != self.device:
             raise ValueError("the two caches must be on the same device")
-        with _On(self.device, stream) as s:
-            check(self.lib.mk_pages_copy(self._ref, src._ref, _ints(src_pages, "src_pages", (n,), self.device),
-                                         _ints(dst_pages, "dst_pages", (n,), self.device), n, s),
-                  None, "mk_pages_copy", op=True)
+        self._call("mk_pages_copy", stream, src._ref, self._list("src_pages", src_pages, n),
+                   self._list("dst_pages", dst_pages, n), n)
 
     def check(self, stream=None) -> None:
         """Raise MkError for the first error the cache's kernels met since the
         last check (waits for the stream)."""
-        with _On(self.device, stream) as s:
-            check(self.lib.mk_pages_status(self._ref, s), None, "mk_pages_status", op=True)
+        self._call("mk_pages_status", stream)
 
 
 def tree_mask(parents: torch.Tensor) -> torch.Tensor:
@@ -184,10 +189,10 @@ def _tokens(x: torch.Tensor, name: str, shape: tuple, dtypes, device: torch.devi
     """Checks a [n, T, ...] tensor whose tokens are dense rows at one stride;
     returns that stride in elements."""
     n, T = shape[:2]
-    if tuple(x.shape) != shape or x.dtype not in dtypes or x.device != device:
+    if x.shape != shape or x.dtype not in dtypes or x.device != device:
         raise ValueError(f"{name} must be {list(shape)} of {' or '.join(str(t) for t in dtypes)} on {device}")
-    if x.is_contiguous():
-        return x.numel() // max(1, n * T) if n * T else _numel(shape[2:])
+    if x.is_contiguous() and n * T:
+        return x.numel() // (n * T)
     width = 1
     for k in range(x.dim() - 1, 1, -1):
         if x.shape[k] != 1 and x.stride(k) != width:
@@ -197,13 +202,6 @@ def _tokens(x: torch.Tensor, name: str, shape: tuple, dtypes, device: torch.devi
     if n > 1 and T > 1 and x.stride(0) != T * step:
         raise ValueError(f"{name}: tokens must be at one stride")
     return step
-
-
-def _numel(shape) -> int:
-    k = 1
-    for s in shape:
-        k *= s
-    return k
 
 
 def qk_norm_rope(qkv: torch.Tensor, cache: PagedCache, layer: int, seqs: torch.Tensor, n_heads: int, theta: float,
@@ -224,15 +222,18 @@ def qk_norm_rope(qkv: torch.Tensor, cache: PagedCache, layer: int, seqs: torch.T
     for g in (q_gain, k_gain):
         if g is not None and (g.dtype != torch.bfloat16 or g.shape != (d,) or g.device != dev or not g.is_contiguous()):
             raise ValueError("gains must be contiguous bf16 [head_dim]")
-    with _On(dev, stream) as s:
-        if out is None:
-            out = torch.empty((n, T, n_heads, d), dtype=cache.dtype, device=dev)
-        check(cache.lib.mk_qk_norm_rope(
-            cache._ref, layer, qkv.data_ptr(), _TYPES[qkv.dtype], stride, n, T, n_heads,
-            _ints(seqs, "seqs", (n,), dev), _ints(n_new, "n_new", (n,), dev), _ints(depth, "depth", (n, T), dev),
-            None if q_gain is None else q_gain.data_ptr(), None if k_gain is None else k_gain.data_ptr(), eps, theta,
-            out.data_ptr(), _tokens(out, "out", (n, T, n_heads, d), (cache.dtype,), dev), s),
-            None, "mk_qk_norm_rope", op=True)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return qk_norm_rope(qkv, cache, layer, seqs, n_heads, theta, q_gain, k_gain, eps, n_new, depth, out)
+    if out is None:
+        out = torch.empty((n, T, n_heads, d), dtype=cache.dtype, device=dev)
+    st = cache.lib.mk_qk_norm_rope(
+        cache._ref, layer, qkv.data_ptr(), _TYPES[qkv.dtype], stride, n, T, n_heads, _ints(seqs, "seqs", (n,), dev),
+        _ints(n_new, "n_new", (n,), dev), _ints(depth, "depth", (n, T), dev),
+        None if q_gain is None else q_gain.data_ptr(), None if k_gain is None else k_gain.data_ptr(), eps, theta,
+        out.data_ptr(), _tokens(out, "out", (n, T, n_heads, d), (cache.dtype,), dev), _raw_stream(dev.index))
+    if st:
+        check(st, None, "mk_qk_norm_rope", op=True)
     return out
 
 
@@ -252,19 +253,22 @@ def attention_tree(q: torch.Tensor, cache: PagedCache, layer: int, seqs: torch.T
     dev = cache.device
     shape = (n, T, nq, cache.head_dim)
     stride = _tokens(q, "q", shape, (cache.dtype,), dev)
-    with _On(dev, stream) as s:
-        if out is None:
-            out = torch.empty(shape, dtype=cache.dtype, device=dev)
-        elif out.data_ptr() == q.data_ptr():
-            raise ValueError("out must not be q")
-        if scratch is None:
-            scratch = torch.empty(cache.lib.mk_attention_tree_scratch_bytes(T, nq, cache.n_kv_heads, d),
-                                  dtype=torch.uint8, device=dev)
-        elif scratch.device != dev or not scratch.is_contiguous():
-            raise ValueError("scratch must be a contiguous tensor on the cache's device")
-        check(cache.lib.mk_attention_tree(
-            cache._ref, layer, q.data_ptr(), stride, n, T, nq, _ints(seqs, "seqs", (n,), dev),
-            _ints(n_new, "n_new", (n,), dev), _ints(mask, "mask", (n, T, (T + 31) // 32), dev), out.data_ptr(),
-            _tokens(out, "out", shape, (cache.dtype,), dev), scratch.data_ptr(),
-            scratch.numel() * scratch.element_size(), s), None, "mk_attention_tree", op=True)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return attention_tree(q, cache, layer, seqs, n_new, mask, out, scratch)
+    if out is None:
+        out = torch.empty(shape, dtype=cache.dtype, device=dev)
+    elif out.data_ptr() == q.data_ptr():
+        raise ValueError("out must not be q")
+    if scratch is None:
+        scratch = torch.empty(cache._scratch_bytes(T, nq), dtype=torch.uint8, device=dev)
+    elif scratch.device != dev or not scratch.is_contiguous():
+        raise ValueError("scratch must be a contiguous tensor on the cache's device")
+    st = cache.lib.mk_attention_tree(
+        cache._ref, layer, q.data_ptr(), stride, n, T, nq, _ints(seqs, "seqs", (n,), dev),
+        _ints(n_new, "n_new", (n,), dev), _ints(mask, "mask", (n, T, (T + 31) // 32), dev), out.data_ptr(),
+        _tokens(out, "out", shape, (cache.dtype,), dev), scratch.data_ptr(),
+        scratch.numel() * scratch.element_size(), _raw_stream(dev.index))
+    if st:
+        check(st, None, "mk_attention_tree", op=True)
     return out
