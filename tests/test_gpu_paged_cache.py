@@ -278,6 +278,29 @@ def test_norm_rope_append_matches_64_bits(lengths, T, nq, nkv, d, ps, dtype, src
     assert torch.equal(got, pool.kv)  # nothing else was written
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("only", ["q", "k"])
+def test_a_gain_for_one_of_q_and_k(d, only):
+    """3 q heads and 1 KV head: q and k heads side by side in a warp, one normed."""
+    import tile_synchronised_b200 as mk
+    g = generator(35)
+    T, nq = 6, 3
+    pool = filled([9], [T], nkv=1, d=d, seed=36, poison=False)
+    cache = pool.to_cache()
+    qkv = torch.randn((1, T, (nq + 2) * d), generator=g)
+    gain = (1 + 0.2 * torch.randn(d, generator=g)).to(torch.bfloat16)
+    gains = (gain, None) if only == "q" else (None, gain)
+    q = mk.qk_norm_rope(qkv.cuda(), cache, 0, ints(0), nq, 10000.0, *(None if x is None else x.cuda() for x in gains))
+    cache.check()
+    ref, bound, kv = rope_reference(pool, 0, qkv, nq, 10000.0, *gains, 1e-6, [0], [T], None, torch.zeros_like(q.cpu()))
+    assert ((q.cpu().double() - ref).abs() <= bound).all()
+    got = cache.kv.cpu()
+    for (i, t), (k, v, kb) in kv.items():
+        page, off = pool.at(0, 9 + t)
+        assert ((got[0, 0, page, :, off].double() - k).abs() <= kb).all()
+        assert torch.equal(got[1, 0, page, :, off], v.to(torch.bfloat16))
+
+
 def test_zero_and_tiny_heads():
     """A head of zeros stays zero under the norm, without a NaN."""
     import tile_synchronised_b200 as mk

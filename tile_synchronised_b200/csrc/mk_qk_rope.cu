@@ -8,10 +8,13 @@
 //
 // The angle is kept in turns in 64 bits (position * theta^(-2i/d) / 2 pi,
 // reduced by its nearest integer), so that far positions lose nothing; sine
-// and cosine then are of a number within half a turn, in 32 bits.  One CTA
-// per token: its d/2 sines and cosines are computed once for all heads.
-// A warp takes a head at a time, each lane the same d/64 values of both
-// halves, so a rotation needs no exchange and the norm one warp sum.
+// and cosine then are of a number within half a turn, in 32 bits.  A CTA takes
+// kRopeTokens tokens of a sequence (one where there are too few to fill the
+// SMs): their sines and cosines are computed once for all heads.  D / 8 lanes
+// take a head, 4 values of both halves each, so that a rotation needs no
+// exchange, the norm one sum over those lanes, and loads are of 16 bytes; they
+// go through the heads kRopeRows at a time.  The first loads go out before the
+// chain sequence -> length -> page -> holders is followed.
 // Bound by HBM: each input value is read once (4 or 2 bytes), each output
 // written once (2 bytes).
 #include <atomic>
@@ -22,7 +25,7 @@
 
 namespace mk {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 256, kRopeTokens = 4, kRopeRows = 3;
 
 struct RopeArgs {
     mk_pages p;
@@ -37,135 +40,144 @@ struct RopeArgs {
     double log2_theta;
 };
 
-// E consecutive values of 32 or 16 bits, widened.
-template <int E, bool F32, bool BF16>
-__device__ __forceinline__ void load_values(const void *base, size_t at, float *v) {
+// 4 consecutive values of 32 or 16 bits, widened.
+template <bool F32, bool BF16>
+__device__ __forceinline__ float4 load4(const void *base, size_t at) {
     if constexpr (F32) {
-        const float *s = static_cast<const float *>(base) + at;
-        if constexpr (E == 4) {
-            const float4 x = *reinterpret_cast<const float4 *>(s);
-            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-        } else if constexpr (E == 2) {
-            const float2 x = *reinterpret_cast<const float2 *>(s);
-            v[0] = x.x, v[1] = x.y;
-        } else {
-            v[0] = s[0];
-        }
+        return *reinterpret_cast<const float4 *>(static_cast<const float *>(base) + at);
     } else {
-        const uint16_t *s = static_cast<const uint16_t *>(base) + at;
-        if constexpr (E == 4) {
-            const uint2 x = *reinterpret_cast<const uint2 *>(s);
-            v[0] = from16<BF16>(x.x & 0xFFFF), v[1] = from16<BF16>(x.x >> 16);
-            v[2] = from16<BF16>(x.y & 0xFFFF), v[3] = from16<BF16>(x.y >> 16);
-        } else if constexpr (E == 2) {
-            const uint32_t x = *reinterpret_cast<const uint32_t *>(s);
-            v[0] = from16<BF16>(x & 0xFFFF), v[1] = from16<BF16>(x >> 16);
-        } else {
-            v[0] = from16<BF16>(s[0]);
-        }
+        const uint2 x = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(base) + at);
+        return make_float4(from16<BF16>(x.x & 0xFFFF), from16<BF16>(x.x >> 16), from16<BF16>(x.y & 0xFFFF),
+                           from16<BF16>(x.y >> 16));
     }
 }
+template <bool BF16>
+__device__ __forceinline__ void store4(uint16_t *to, const float4 &v) {
+    *reinterpret_cast<uint2 *>(to) = make_uint2(pack16<BF16>(v.x, v.y), pack16<BF16>(v.z, v.w));
+}
+__device__ __forceinline__ float dot4(const float4 &x, const float4 &y) {
+    return fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, x.w * y.w)));
+}
+__device__ __forceinline__ float4 mul4(const float4 &x, const float4 &y) {
+    return make_float4(x.x * y.x, x.y * y.y, x.z * y.z, x.w * y.w);
+}
+__device__ __forceinline__ float4 scale4(const float4 &x, float s) {
+    return make_float4(x.x * s, x.y * s, x.z * s, x.w * s);
+}
 
-template <int E, bool BF16>
-__device__ __forceinline__ void store_values(uint16_t *to, const float *v) {
-    if constexpr (E == 4)
-        *reinterpret_cast<uint2 *>(to) = make_uint2(pack16<BF16>(v[0], v[1]), pack16<BF16>(v[2], v[3]));
-    else if constexpr (E == 2)
-        *reinterpret_cast<uint32_t *>(to) = pack16<BF16>(v[0], v[1]);
-    else
-        to[0] = to16<BF16>(v[0]);
+template <int D, bool F32, bool BF16, int TOK>
+__global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(const __grid_constant__ RopeArgs a) {
+    constexpr int LR = D / 8, kSubs = kRopeThreads / LR;  // lanes of a head, heads at a time
+    __shared__ float s_cos[TOK][D / 2], s_sin[TOK][D / 2];
+    __shared__ size_t s_row[TOK];  // offset of the token's slot in its layer's K or V
+    __shared__ int s_write[TOK];
+    const int chunks = (a.T + TOK - 1) / TOK, i = blockIdx.x / chunks, t0 = (blockIdx.x - i * chunks) * TOK;
+    const int sub = threadIdx.x / LR, at = threadIdx.x % LR * 4;  // first head, values at, at + D / 2 of each
+    const int nkv = a.p.n_kv_heads, heads = a.nq + 2 * nkv;
+    float4 lo[kRopeRows], hi[kRopeRows];
+    auto load = [&](int t, int h0) {  // heads h0 + sub, ... of token t
+        const size_t row = (size_t)(i * a.T + t0 + t) * a.qkv_stride + at;
+#pragma unroll
+        for (int x = 0; x < kRopeRows; ++x) {
+            const int h = h0 + sub + x * kSubs;
+            if (h < heads) {
+                lo[x] = load4<F32, BF16>(a.qkv, row + (size_t)h * D);
+                hi[x] = load4<F32, BF16>(a.qkv, row + (size_t)h * D + D / 2);
+            }
+        }
+    };
+    load(0, 0);
+
+    const PagesEntry e = pages_entry(a.p, a.seqs, a.n_new, i, a.T);
+    const int tokens = min(TOK, e.fresh - t0);  // the others are padding, or the entry is out of range
+    if (tokens <= 0) {
+        if (e.err && t0 == 0 && threadIdx.x == 0) pages_fail(a.p.state, e.err, i, e.seq);
+        return;
+    }
+    int twice = 0;
+    for (int k = threadIdx.x; k < a.n; k += kRopeThreads) twice |= k != i && a.seqs[k] == e.seq;
+    twice = __syncthreads_or(twice);
+    if (threadIdx.x < tokens) {  // the slot of the new token, and whether it may be written
+        const int slot = e.len + t0 + threadIdx.x;
+        const int page = a.p.table[(size_t)e.seq * a.p.max_pages + slot / a.p.page_size];
+        int err = 0;
+        if (twice)
+            err = kPgSeq;
+        else if (page < 0 || page >= a.p.n_pages)
+            err = kPgPosition;
+        else if (a.p.refs[page] != 1)
+            err = kPgShared;
+        if (err) pages_fail(a.p.state, err, i, err == kPgSeq ? e.seq : page);
+        s_write[threadIdx.x] = !err;
+        s_row[threadIdx.x] = ((size_t)(err ? 0 : page) * nkv * a.p.page_size + slot % a.p.page_size) * D;
+    }
+    for (int x = threadIdx.x; x < tokens * (D / 2); x += kRopeThreads) {
+        const int t = x / (D / 2), j = x - t * (D / 2);
+        const long long pos = (long long)e.len + (a.depth ? a.depth[i * a.T + t0 + t] : t0 + t);
+        // theta^(-2j/d) / 2 pi
+        const double turns = (double)pos * exp2(a.log2_theta * (-2.0 * j / D) - 2.6514961294723188);
+        sincospif((float)(2.0 * (turns - rint(turns))), &s_sin[t][j], &s_cos[t][j]);
+    }
+    __syncthreads();
+    uint16_t *const kv = static_cast<uint16_t *>(a.p.kv);
+#pragma unroll 1
+    for (int t = 0; t < tokens; ++t) {
+        const float4 c = *reinterpret_cast<const float4 *>(&s_cos[t][at]);
+        const float4 s = *reinterpret_cast<const float4 *>(&s_sin[t][at]);
+#pragma unroll 1
+        for (int h0 = 0; h0 < heads; h0 += kRopeRows * kSubs) {
+            if (t || h0) load(t, h0);
+#pragma unroll
+            for (int x = 0; x < kRopeRows; ++x) {
+                const int h = h0 + sub + x * kSubs;
+                const bool is_q = h < a.nq, is_v = h >= a.nq + nkv;
+                const uint16_t *gain = is_q ? a.q_gain : a.k_gain;
+                float4 l = lo[x], u = hi[x];
+                if (a.q_gain || a.k_gain) {  // every lane of the warp: the sum needs them all
+                    float ss = h < heads && !is_v ? dot4(l, l) + dot4(u, u) : 0.f;
+#pragma unroll
+                    for (int o = LR / 2; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+                    const float n = rsqrtf(ss * (1.f / D) + a.eps);
+                    if (gain && !is_v) {
+                        l = mul4(scale4(l, n), load4<false, true>(gain, at));
+                        u = mul4(scale4(u, n), load4<false, true>(gain, at + D / 2));
+                    }
+                }
+                if (h >= heads || (!is_q && !s_write[t])) continue;
+                if (!is_v) {
+                    const float4 v = l;
+                    l = make_float4(v.x * c.x - u.x * s.x, v.y * c.y - u.y * s.y, v.z * c.z - u.z * s.z,
+                                    v.w * c.w - u.w * s.w);
+                    u = make_float4(u.x * c.x + v.x * s.x, u.y * c.y + v.y * s.y, u.z * c.z + v.z * s.z,
+                                    u.w * c.w + v.w * s.w);
+                }
+                uint16_t *to = is_q ? a.q + (size_t)(i * a.T + t0 + t) * a.q_stride + (size_t)h * D
+                                    : kv + (is_v ? a.v_off : a.k_off) + s_row[t] +
+                                          (size_t)(h - a.nq - (is_v ? nkv : 0)) * a.p.page_size * D;
+                store4<BF16>(to + at, l);
+                store4<BF16>(to + at + D / 2, u);
+            }
+        }
+    }
 }
 
 template <int D, bool F32, bool BF16>
-__global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(const RopeArgs a) {
-    constexpr int E = D / 64;  // values of each half per lane
-    __shared__ float s_cos[D / 2], s_sin[D / 2];
-    const int tok = blockIdx.x, i = tok / a.T, t = tok - i * a.T;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const PagesEntry e = pages_entry(a.p, a.seqs, a.n_new, i, a.T);
-    int twice = 0;
-    for (int k = threadIdx.x; k < a.n; k += kRopeThreads) twice |= k != i && a.seqs[k] == e.seq;
-    if (t >= e.fresh) {  // padding, or an entry that is out of range
-        if (e.err && t == 0 && threadIdx.x == 0) pages_fail(a.p.state, e.err, i, e.seq);
-        return;
-    }
-    const long long pos = (long long)e.len + (a.depth ? a.depth[tok] : t);
-    if (threadIdx.x < D / 2) {
-        const double turns = (double)pos * exp2(a.log2_theta * (-2.0 * threadIdx.x / D) - 2.6514961294723188);
-        sincospif((float)(2.0 * (turns - rint(turns))), &s_sin[threadIdx.x], &s_cos[threadIdx.x]);
-    }
-    twice = __syncthreads_or(twice);
-    // the slot of the new token, and whether it may be written
-    const int slot = e.len + t;
-    const int page = a.p.table[(size_t)e.seq * a.p.max_pages + slot / a.p.page_size];
-    int err = 0;
-    if (twice)
-        err = kPgSeq;
-    else if (page < 0 || page >= a.p.n_pages)
-        err = kPgPosition;
-    else if (a.p.refs[page] != 1)
-        err = kPgShared;
-    if (err && threadIdx.x == 0) pages_fail(a.p.state, err, i, err == kPgSeq ? e.seq : page);
-    const int nkv = a.p.n_kv_heads;
-    const size_t row = ((size_t)(err ? 0 : page) * nkv * a.p.page_size + slot % a.p.page_size) * D;
-    float c[E], s[E], gq[2][E], gk[2][E];
-#pragma unroll
-    for (int x = 0; x < E; ++x) {
-        c[x] = s_cos[lane * E + x];
-        s[x] = s_sin[lane * E + x];
-    }
-    if (a.q_gain) {
-        load_values<E, false, true>(a.q_gain, lane * E, gq[0]);
-        load_values<E, false, true>(a.q_gain, D / 2 + lane * E, gq[1]);
-    }
-    if (a.k_gain) {
-        load_values<E, false, true>(a.k_gain, lane * E, gk[0]);
-        load_values<E, false, true>(a.k_gain, D / 2 + lane * E, gk[1]);
-    }
-    const int heads = err ? a.nq : a.nq + 2 * nkv;
-    for (int h = warp; h < heads; h += kRopeThreads / 32) {
-        const size_t at = (size_t)tok * a.qkv_stride + (size_t)h * D + lane * E;
-        float lo[E], hi[E];
-        load_values<E, F32, BF16>(a.qkv, at, lo);
-        load_values<E, F32, BF16>(a.qkv, at + D / 2, hi);
-        uint16_t *to;
-        if (h < a.nq + nkv) {
-            const bool is_q = h < a.nq;
-            if (is_q ? a.q_gain != nullptr : a.k_gain != nullptr) {
-                float ss = 0.f;
-#pragma unroll
-                for (int x = 0; x < E; ++x) ss = fmaf(lo[x], lo[x], fmaf(hi[x], hi[x], ss));
-                const float r = rsqrtf(warp_sum(ss) * (1.f / D) + a.eps);
-#pragma unroll
-                for (int x = 0; x < E; ++x) {
-                    lo[x] *= r * (is_q ? gq[0][x] : gk[0][x]);
-                    hi[x] *= r * (is_q ? gq[1][x] : gk[1][x]);
-                }
-            }
-#pragma unroll
-            for (int x = 0; x < E; ++x) {
-                const float u = lo[x], w = hi[x];
-                lo[x] = u * c[x] - w * s[x];
-                hi[x] = w * c[x] + u * s[x];
-            }
-            to = is_q ? a.q + (size_t)tok * a.q_stride + (size_t)h * D
-                      : static_cast<uint16_t *>(a.p.kv) + a.k_off + row + (size_t)(h - a.nq) * a.p.page_size * D;
-        } else {
-            to = static_cast<uint16_t *>(a.p.kv) + a.v_off + row + (size_t)(h - a.nq - nkv) * a.p.page_size * D;
-        }
-        store_values<E, BF16>(to + lane * E, lo);
-        store_values<E, BF16>(to + D / 2 + lane * E, hi);
-    }
+static void launch_rope_as(const RopeArgs &a, cudaStream_t s) {
+    // 4 tokens a CTA once that still gives every SM two
+    if ((long long)a.n * a.T >= 2 * kRopeTokens * pages_sms())
+        qk_rope_kernel<D, F32, BF16, kRopeTokens>
+            <<<(unsigned)(a.n * ((a.T + kRopeTokens - 1) / kRopeTokens)), kRopeThreads, 0, s>>>(a);
+    else
+        qk_rope_kernel<D, F32, BF16, 1><<<(unsigned)(a.n * a.T), kRopeThreads, 0, s>>>(a);
 }
 
 template <int D>
 static cudaError_t launch_rope(const RopeArgs &a, bool f32, cudaStream_t s) {
-    const unsigned grid = (unsigned)(a.n * a.T);
     const bool bf16 = a.p.dtype == MK_BF16;
-    if (f32 && bf16) qk_rope_kernel<D, true, true><<<grid, kRopeThreads, 0, s>>>(a);
-    if (f32 && !bf16) qk_rope_kernel<D, true, false><<<grid, kRopeThreads, 0, s>>>(a);
-    if (!f32 && bf16) qk_rope_kernel<D, false, true><<<grid, kRopeThreads, 0, s>>>(a);
-    if (!f32 && !bf16) qk_rope_kernel<D, false, false><<<grid, kRopeThreads, 0, s>>>(a);
+    if (f32 && bf16) launch_rope_as<D, true, true>(a, s);
+    if (f32 && !bf16) launch_rope_as<D, true, false>(a, s);
+    if (!f32 && bf16) launch_rope_as<D, false, true>(a, s);
+    if (!f32 && !bf16) launch_rope_as<D, false, false>(a, s);
     return cudaGetLastError();
 }
 
