@@ -57,7 +57,7 @@ namespace mk {
 
 constexpr int kTreeM = 128;          // rows of an MMA
 constexpr int kTreeMaxStages = 12;
-constexpr int kTreeMaxCtas = 256;    // of the grid, and so records of an item
+constexpr int kTreeMaxCtas = 192;    // of the grid, and so records of an item
 
 // Softmax groups and positions of a tile at head size d.
 __host__ __device__ constexpr int tree_groups(int d) { return d == 256 ? 1 : 2; }
@@ -288,6 +288,17 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
     return r;
+}
+
+// Is the phase `parity` of an mbarrier complete?  (Does not wait.)
+__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 // True in one lane of the warp.
@@ -565,22 +576,23 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
             const int nt = __shfl_sync(0xFFFFFFFFu, run.t1 - run.t0, 0);
             const bool two = __shfl_sync(0xFFFFFFFFu, (int)two_rows(), 0);
             const int jobs = two ? 2 * nt : nt;
-            auto qk = [&](int j) {
+            auto qk_issue = [&](int j) {  // by the elected lane, once K is there
                 const int b = j & 1;
+                const uint64_t dk = d_k + (uint32_t)k_slot * (kStage >> 4), dq = d_q + (two && b ? kQBytes >> 4 : 0);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    tc_mma(tmem + (uint32_t)b * 128, dq + (ks / 4) * (kTreeM * 8) + (ks % 4) * 2,
+                           dk + (ks / 4) * (NT * 8) + (ks % 4) * 2, id_qk, ks > 0);
+                tc_commit(&sh.s_full[b]);
+                if (!two || b) tc_commit(&sh.empty[k_slot]);
+                if (j == jobs - 1) tc_commit(&sh.q_empty);
+            };
+            auto qk = [&](int j) {
                 if (!__all_sync(0xFFFFFFFFu, tc_wait(&sh.full[k_slot], k_phase, abort))) return false;
                 tc_fence_after();
-                const uint64_t dk = d_k + (uint32_t)k_slot * (kStage >> 4), dq = d_q + (two && b ? kQBytes >> 4 : 0);
-                if (elect_one()) {
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)
-                        tc_mma(tmem + (uint32_t)b * 128, dq + (ks / 4) * (kTreeM * 8) + (ks % 4) * 2,
-                               dk + (ks / 4) * (NT * 8) + (ks % 4) * 2, id_qk, ks > 0);
-                    tc_commit(&sh.s_full[b]);
-                    if (!two || b) tc_commit(&sh.empty[k_slot]);
-                    if (j == jobs - 1) tc_commit(&sh.q_empty);
-                }
+                if (elect_one()) qk_issue(j);
                 __syncwarp();
-                if (!two || b) step(k_slot, k_phase);
+                if (!two || (j & 1)) step(k_slot, k_phase);
                 return true;
             };
             ok = __all_sync(0xFFFFFFFFu, tc_wait(&sh.q_full, seg_no & 1u, abort));
@@ -589,6 +601,8 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
 #pragma unroll 1
             for (int j = 0; ok && j < jobs; ++j) {
                 const int b = j & 1;
+                // With K of job j + 2 there already, its S goes out right behind P V
+                const bool k_there = __all_sync(0xFFFFFFFFu, j + 2 < jobs && mbar_test_wait(&sh.full[k_slot], k_phase));
                 ok = tc_wait(&sh.full[v_slot], v_phase, abort) && tc_wait(&sh.p_full[b], used[b] & 1u, abort);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
@@ -603,10 +617,15 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
                     // the softmax waits for P V where it changes O (one group), and at the end of the run
                     if (NG == 1 || j + 2 >= jobs) tc_commit(&sh.pv_done[NG == 2 ? b : 0]);
                     if (!two || b) tc_commit(&sh.empty[v_slot]);
+                    if (k_there) qk_issue(j + 2);
                 }
                 __syncwarp();
                 if (!two || b) step(v_slot, v_phase);
-                if (j + 2 < jobs) ok = qk(j + 2);
+                if (k_there) {
+                    if (!two || b) step(k_slot, k_phase);
+                } else if (j + 2 < jobs) {
+                    ok = qk(j + 2);
+                }
             }
             ++seg_no;
         }
@@ -642,13 +661,24 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
                 if (!ok) break;
                 ++seen[b];
                 tc_fence_after();
-                float lo[32], hi[32];  // 32 scores each
-                float top = 0.f;
+                // Two passes over S, for its maximum and for P, 64 scores at a
+                // time.  Rolled loops: unrolled, the compiler's schedule
+                // overflows the registers, and there is hardly an L1 to spill to.
+                float lo[32], hi[32], top = -CUDART_INF_F;
                 auto hide = [&](float *v, uint32_t w) {
                     if (tail && __any_sync(0xFFFFFFFFu, w != 0xFFFFFFFFu)) {
+                        asm volatile("" : "+r"(w));  // else the bit tests are kept from pass to pass
 #pragma unroll
                         for (int k = 0; k < 32; ++k) v[k] = (w >> k) & 1u ? v[k] : -CUDART_INF_F;
                     }
+                };
+                auto read = [&](int c) {
+                    tmem_ld32(sc + c, lo);
+                    tmem_ld32(sc + c + 32, hi);
+                    tmem_wait_ld(lo);
+                    tmem_wait_ld(hi);
+                    hide(lo, c ? bits[NT / 32 - 2] : bits[0]);
+                    hide(hi, c ? bits[NT / 32 - 1] : bits[1]);
                 };
                 auto max32 = [&](const float *v) {
                     float x[4] = {v[0], v[1], v[2], v[3]};
@@ -657,17 +687,10 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
                     return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
                 };
                 if (warp_live) {
-                    // the upper half of 128 scores first; the lower stays in registers
-#pragma unroll
+#pragma unroll 1
                     for (int c = NT - 64; c >= 0; c -= 64) {
-                        tmem_ld32(sc + c, lo);
-                        tmem_ld32(sc + c + 32, hi);
-                        tmem_wait_ld(lo);
-                        hide(lo, bits[c / 32]);
-                        top = c == NT - 64 ? max32(lo) : fmaxf(top, max32(lo));
-                        tmem_wait_ld(hi);
-                        hide(hi, bits[c / 32 + 1]);
-                        top = fmaxf(top, max32(hi));
+                        read(c);
+                        top = max3(top, max32(lo), max32(hi));
                     }
                 }
                 if (NG == 1 && i > 0) {  // P V of the last tile (two groups: S came after it)
@@ -715,18 +738,13 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
                         }
                         tmem_st16(to, pk);
                     };
-                    // P goes over S from the front: over scores in registers, or used up
-                    exps(lo, sc);
-                    if constexpr (NT == 128) tmem_ld32(sc + 64, lo);
-                    exps(hi, sc + 16);
-                    if constexpr (NT == 128) {
-                        tmem_ld32(sc + 96, hi);
-                        tmem_wait_ld(lo);
-                        hide(lo, bits[2]);
-                        exps(lo, sc + 32);
-                        tmem_wait_ld(hi);
-                        hide(hi, bits[3]);
-                        exps(hi, sc + 48);
+                    // P goes over S from the front: over scores in registers, or used
+                    // up; the first pass left the first 64 in registers
+#pragma unroll 1
+                    for (int c = 0; c < NT; c += 64) {
+                        if (c) read(c);
+                        exps(lo, sc + c / 2);
+                        exps(hi, sc + c / 2 + 16);
                     }
                     float x, y;
                     unpair(add2(sum0, sum1), x, y);
@@ -834,14 +852,14 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
 }
 
 // Joins the records of every item that more than one CTA worked on: CTA
-// (x, i, g) 8 rows of an item of KV head g of entry i, a thread 4 columns of
-// one row (the 8 rows of a column block are side by side in a record).
-constexpr int kCombineRows = 8;
+// (x, i, g) 8 R rows of an item of KV head g of entry i, a thread 4 columns of
+// R rows (8 rows of a column block are side by side in a record).  R = 4 where
+// that leaves CTAs enough: a CTA takes some 3 us whatever it finds to join.
 constexpr int kCombineThreads = 256;
 
-template <int D, bool BF16>
+template <int D, bool BF16, int R>
 __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const __grid_constant__ TreeArgs a, int grid) {
-    constexpr int NT = tree_nt(D), NG = tree_groups(D);
+    constexpr int NT = tree_nt(D), NG = tree_groups(D), kCombineRows = 8 * R;
     __shared__ long long s_red[2][kCombineThreads / 32];
     __shared__ float s_w[kTreeMaxCtas][kCombineRows];  // weight of each record's row
     __shared__ float s_inv[kCombineRows];
@@ -888,41 +906,56 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const __g
     pdl_wait();              // the records are complete
     if (c0 == c1) return;    // none, or the item's only CTA wrote the result
     auto slot = [&](int c) { return (size_t)(c == 0 ? slot0 : 2 * (c0 + c)); };
-    // warp = row: its maximum, the weights and the sum
-    if (r0 + warp < a.rows_cap) {
+    // a warp takes R rows, 32 / R lanes each: maximum, weights and sum
+    {
+        constexpr int kL = 32 / R;
+        const int x = warp * R + lane / kL, c_first = lane % kL;
+        const bool real = r0 + x < a.rows_cap;
         float M = -CUDART_INF_F, L = 0.f;
-        for (int c = lane; c < count; c += 32) M = fmaxf(M, a.part_ml[slot(c) * a.rows_cap + r0 + warp].x);
-        M = warp_max(M);
+        for (int c = c_first; real && c < count; c += kL) M = fmaxf(M, a.part_ml[slot(c) * a.rows_cap + r0 + x].x);
+#pragma unroll
+        for (int o = kL / 2; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
         if (M == -CUDART_INF_F) M = 0.f;
-        for (int c = lane; c < count; c += 32) {
-            const float2 ml = a.part_ml[slot(c) * a.rows_cap + r0 + warp];
+        for (int c = c_first; real && c < count; c += kL) {
+            const float2 ml = a.part_ml[slot(c) * a.rows_cap + r0 + x];
             const float f = ex2(ml.x - M);
-            s_w[c][warp] = f;
+            s_w[c][x] = f;
             L = fmaf(f, ml.y, L);
         }
-        L = warp_sum(L);
-        if (lane == 0) s_inv[warp] = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+        for (int o = kL / 2; o; o >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, o);
+        if (c_first == 0) s_inv[x] = L == 0.f ? 0.f : 1.f / L;
     }
     __syncthreads();
-    const int r = r0 + (lane & 7), gt = r & (kTreeM - 1), t = (rt * NG + r / kTreeM) * a.toks + gt / a.G;
-    if (r >= a.rows_cap || gt >= a.toks * a.G || t >= e.fresh) return;
-    const float inv = s_inv[lane & 7];
-    uint16_t *to = a.out + ((size_t)i * a.T + t) * a.out_stride + (size_t)(g * a.G + gt % a.G) * D;
+    const size_t pitch = (size_t)(D / 4) * a.rows_cap;
     for (int c4 = warp * 4 + (lane >> 3); c4 < D / 4; c4 += kCombineThreads / 8) {
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        const float4 *rec = a.part_o + (size_t)c4 * a.rows_cap + r;
-        const size_t pitch = (size_t)(D / 4) * a.rows_cap;
-#pragma unroll 8
+        const float4 *rec = a.part_o + (size_t)c4 * a.rows_cap + r0 + (lane & 7);
+        float4 o[R];
+#pragma unroll
+        for (int x = 0; x < R; ++x) o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll(R == 1 ? 8 : 2)
         for (int c = 0; c < count; ++c) {
-            const float4 v = rec[slot(c) * pitch];
-            const float f = s_w[c][lane & 7];
-            o.x = fmaf(f, v.x, o.x);
-            o.y = fmaf(f, v.y, o.y);
-            o.z = fmaf(f, v.z, o.z);
-            o.w = fmaf(f, v.w, o.w);
+            const float4 *at = rec + slot(c) * pitch;
+#pragma unroll
+            for (int x = 0; x < R; ++x) {
+                if (r0 + 8 * x + (lane & 7) >= a.rows_cap) continue;
+                const float4 v = at[8 * x];
+                const float f = s_w[c][8 * x + (lane & 7)];
+                o[x].x = fmaf(f, v.x, o[x].x);
+                o[x].y = fmaf(f, v.y, o[x].y);
+                o[x].z = fmaf(f, v.z, o[x].z);
+                o[x].w = fmaf(f, v.w, o[x].w);
+            }
         }
-        *reinterpret_cast<uint2 *>(to + c4 * 4) =
-            make_uint2(pack16<BF16>(o.x * inv, o.y * inv), pack16<BF16>(o.z * inv, o.w * inv));
+#pragma unroll
+        for (int x = 0; x < R; ++x) {
+            const int r = r0 + 8 * x + (lane & 7), gt = r & (kTreeM - 1), t = (rt * NG + r / kTreeM) * a.toks + gt / a.G;
+            if (r >= a.rows_cap || gt >= a.toks * a.G || t >= e.fresh) continue;
+            const float inv = s_inv[8 * x + (lane & 7)];
+            uint16_t *to = a.out + ((size_t)i * a.T + t) * a.out_stride + (size_t)(g * a.G + gt % a.G) * D;
+            *reinterpret_cast<uint2 *>(to + c4 * 4) =
+                make_uint2(pack16<BF16>(o[x].x * inv, o[x].y * inv), pack16<BF16>(o[x].z * inv, o[x].w * inv));
+        }
     }
 }
 
@@ -957,9 +990,12 @@ static cudaError_t launch_tree(const CUtensorMap &mq, const CUtensorMap &mk, con
     attn_tree_kernel<D, BF16><<<grid, tree_threads(D), fixed + a.stages * stage, s>>>(mq, mk, mv, a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    // 8 rows a CTA, or 32 once 8 make more CTAs than run at the same time
+    const int item = tree_groups(D) * a.toks, rts = (a.T + item - 1) / item;
+    const auto blocks = [&](int rows) { return (a.rows_cap + rows - 1) / rows; };
+    const bool few = (long long)rts * blocks(8) * a.n * a.p.n_kv_heads <= 6LL * grid;
     cudaLaunchConfig_t cfg = {};
-    const int item = tree_groups(D) * a.toks, blocks = (a.rows_cap + kCombineRows - 1) / kCombineRows;
-    cfg.gridDim = dim3((unsigned)((a.T + item - 1) / item * blocks), (unsigned)a.n, (unsigned)a.p.n_kv_heads);
+    cfg.gridDim = dim3((unsigned)(rts * blocks(few ? 8 : 32)), (unsigned)a.n, (unsigned)a.p.n_kv_heads);
     cfg.blockDim = dim3(kCombineThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -967,7 +1003,8 @@ static cudaError_t launch_tree(const CUtensorMap &mq, const CUtensorMap &mk, con
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_combine_kernel<D, BF16>, a, grid);
+    return few ? cudaLaunchKernelEx(&cfg, tree_combine_kernel<D, BF16, 1>, a, grid)
+               : cudaLaunchKernelEx(&cfg, tree_combine_kernel<D, BF16, 4>, a, grid);
 }
 
 }  // namespace mk
