@@ -212,6 +212,19 @@ def test_wrong_entries_are_left_out_and_reported():
         expect("page index")
 
 
+def test_a_fork_of_a_row_with_a_hole_is_left_undone():
+    import tile_synchronised_b200 as mk
+    for page in (-1, 99):
+        pool = filled([40, 33], [0, 0], layers=1, spare=2, extra=2, poison=False, seed=8)
+        pool.table[0, 1] = page
+        cache = pool.to_cache()
+        cache.fork(ints(0, 1), ints(2, 3))
+        pool.fork([1], [3])
+        with pytest.raises(mk.MkError, match="no page"):
+            cache.check()
+        pool.same_as(cache)
+
+
 def test_operations_in_a_captured_graph():
     """A step's operations captured once, replayed on other lists."""
     pool = filled([20, 33], [0, 0], layers=2, spare=8, extra=1, poison=False, seed=7)

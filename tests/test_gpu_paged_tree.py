@@ -73,6 +73,24 @@ def test_causal_matches_64_bits(lengths, T, nq, nkv, d, ps, dtype):
     run_and_compare(pool, q, list(range(n)), new, None)
 
 
+# Many row tiles of one sequence, each with fewer positions than the next: tokens of a row tile that divide a tile of
+# positions, are more than one, or neither; lengths of zero, one and around a tile.
+CHUNKS = [
+    ([0, 130], 300, 8, 2, 64, 16, torch.bfloat16),    # 64 tokens a row tile, tiles of 128
+    ([1, 77], 260, 6, 2, 128, 48, torch.float16),     # 84 tokens
+    ([127], 520, 1, 1, 64, 128, torch.bfloat16),      # 256 tokens
+    ([5, 64, 0], 150, 7, 1, 256, 32, torch.bfloat16), # 18 tokens, tiles of 64
+    ([63], 37, 128, 1, 64, 64, torch.bfloat16),       # 2 tokens
+]
+
+
+@pytest.mark.parametrize("lengths,T,nq,nkv,d,ps,dtype", CHUNKS)
+def test_long_chunks_match_64_bits(lengths, T, nq, nkv, d, ps, dtype):
+    n = len(lengths)
+    pool, q, new = make(lengths, T, nq, nkv, d, ps, dtype, 31, n_new=[T - 33 * i for i in range(n)])
+    run_and_compare(pool, q, list(range(n)), new, None)
+
+
 def test_many_sequences_in_any_order():
     lengths = [(37 * i) % 211 for i in range(50)]
     pool, q, new = make(lengths, 3, 4, 2, 64, 16, torch.bfloat16, 13)

@@ -29,7 +29,8 @@
 // every tile.  At d = 256 tensor memory holds one O: one group, two S.
 //
 // Work: the units are (sequence, KV head, row tile, tile of positions), the
-// tiles of one row tile consecutive; each CTA (one per SM) takes an equal
+// tiles of one row tile consecutive (without a mask those up to its last
+// token); each CTA (one per SM) takes an equal
 // contiguous range, whatever the lengths, which are only known on the device.
 // A CTA that covers all tiles of an item writes its rows of `out`; else it
 // writes (o, max, sum) to scratch, at most two such records per CTA, and
@@ -40,7 +41,7 @@
 // at a time, ahead); one lane issues the MMAs: with two jobs (tile, group) in
 // flight, S of job j + 2 follows P V of job j.
 //
-// P is rounded to the cache's 16-bit type (2^-9 relative in bf16, each
+// P is rounded to the cache's 16-bit type (2^-8 relative at most in bf16, each
 // element on its own, as V's own storage); S, the maximum, the sum, O and the
 // records are 32 bits.
 #include <cuda.h>
@@ -103,24 +104,54 @@ struct TreeShared {
     int abort, bad_v, pad;
 };
 
-// The units of entry e: KV heads x row tiles x tiles of positions.
+// Row tiles of entry e, and the tiles of positions that row tile rt needs:
+// those up to its last token without a mask, else all.
+template <int D>
+__device__ __forceinline__ int tree_rts(const TreeArgs &a, const TreeEntry &e) {
+    const int item = tree_groups(D) * a.toks;  // new tokens of an item
+    return (e.fresh + item - 1) / item;
+}
+template <int D>
+__device__ __forceinline__ int tree_tiles(const TreeArgs &a, const TreeEntry &e, int rt) {
+    const int last = a.mask ? e.fresh : min(e.fresh, (rt + 1) * tree_groups(D) * a.toks);
+    return (e.len + last + tree_nt(D) - 1) / tree_nt(D);
+}
+// Tiles of row tiles 0 .. rt - 1, rt <= rts.  Without a mask a sum of
+// floor((x i + b) / m), taken with the steps of Euclid's algorithm on (x, m).
+template <int D>
+__device__ __forceinline__ long long tree_before(const TreeArgs &a, const TreeEntry &e, int rt, int rts) {
+    if (a.mask || rts <= 1) return (long long)rt * tree_tiles<D>(a, e, 0);
+    long long sum = rt == rts ? tree_tiles<D>(a, e, rts - 1) : 0;
+    uint32_t n = rt == rts ? rts - 1 : rt, m = tree_nt(D), x = tree_groups(D) * a.toks, b = e.len + x + m - 1;
+    while (n) {
+        sum += (long long)n * (n - 1) / 2 * (x / m) + (long long)n * (b / m);
+        x %= m;
+        b %= m;
+        const uint32_t y = x * n + b;
+        n = y / m;
+        b = y % m;
+        const uint32_t was = m;
+        m = x;
+        x = was;
+    }
+    return sum;
+}
+
+// The units of entry e: tiles of positions x row tiles x KV heads.
 template <int D>
 __device__ __forceinline__ long long tree_units(const TreeArgs &a, const TreeEntry &e) {
-    if (!e.fresh) return 0;
-    const int item = tree_groups(D) * a.toks;  // new tokens of an item
-    const int rts = (e.fresh + item - 1) / item, tiles = (e.len + e.fresh + tree_nt(D) - 1) / tree_nt(D);
-    return (long long)a.p.n_kv_heads * rts * tiles;
+    const int rts = tree_rts<D>(a, e);
+    return e.fresh ? a.p.n_kv_heads * tree_before<D>(a, e, rts, rts) : 0;
 }
 
 // n / d, mostly of small numbers (a 64-bit division takes hundreds of cycles).
-__device__ __forceinline__ long long small_div(long long n, int d) {
-    return n >> 32 ? n / d : (long long)((uint32_t)n / (uint32_t)d);
+__device__ __forceinline__ long long small_div(long long n, long long d) {
+    return (n | d) >> 32 ? n / d : (long long)((uint32_t)n / (uint32_t)d);
 }
 
 // The warp's next run, false at the end of the CTA's range.
 template <int D>
 __device__ __forceinline__ bool tree_next(const TreeArgs &a, TreeRun &r, const long long *pref, const TreeEntry *ent) {
-    constexpr int nt = tree_nt(D);
     __syncwarp();
     if ((threadIdx.x & 31) == 0) {
         r.more = r.u < r.u1;
@@ -130,13 +161,21 @@ __device__ __forceinline__ bool tree_next(const TreeArgs &a, TreeRun &r, const l
             const TreeEntry e = ent[i];
             r.i = i;
             r.e = e;
-            r.tiles = (e.len + e.fresh + nt - 1) / nt;
-            const int rts = (e.fresh + tree_groups(D) * a.toks - 1) / (tree_groups(D) * a.toks);
-            const long long local = r.u - pref[i];
-            const int item = (int)small_div(local, r.tiles);
-            r.t0 = (int)(local - (long long)item * r.tiles);
-            r.g = item / rts;
-            r.rt = item - r.g * rts;
+            const int rts = tree_rts<D>(a, e);
+            const long long head = tree_before<D>(a, e, rts, rts), local = r.u - pref[i];
+            r.g = (int)small_div(local, head);
+            const long long rest = local - r.g * head;
+            int lo = 0, hi = rts;  // the last row tile that starts at or before it
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (tree_before<D>(a, e, mid, rts) <= rest)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            r.rt = lo;
+            r.t0 = (int)(rest - tree_before<D>(a, e, lo, rts));
+            r.tiles = tree_tiles<D>(a, e, lo);
             const long long left = r.u1 - r.u;
             r.t1 = left < r.tiles - r.t0 ? r.t0 + (int)left : r.tiles;
             r.slot = 2 * blockIdx.x + (r.count ? 1 : 0);
@@ -859,7 +898,7 @@ constexpr int kCombineThreads = 256;
 
 template <int D, bool BF16, int R>
 __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const __grid_constant__ TreeArgs a, int grid) {
-    constexpr int NT = tree_nt(D), NG = tree_groups(D), kCombineRows = 8 * R;
+    constexpr int NG = tree_groups(D), kCombineRows = 8 * R;
     __shared__ long long s_red[2][kCombineThreads / 32];
     __shared__ float s_w[kTreeMaxCtas][kCombineRows];  // weight of each record's row
     __shared__ float s_inv[kCombineRows];
@@ -891,10 +930,12 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const __g
         before += s_red[0][k];
         total += s_red[1][k];
     }
-    const int tiles = (e.len + e.fresh + NT - 1) / NT, rts = (e.fresh + NG * a.toks - 1) / (NG * a.toks);
+    const TreeEntry te{e.seq, e.len, e.fresh};
+    const int rts = tree_rts<D>(a, te);
     int c0 = 0, c1 = 0, slot0 = 0;
     if (rt < rts) {
-        const long long u0 = before + ((long long)g * rts + rt) * tiles, u1 = u0 + tiles;
+        const long long u0 = before + g * tree_before<D>(a, te, rts, rts) + tree_before<D>(a, te, rt, rts);
+        const long long u1 = u0 + tree_tiles<D>(a, te, rt);
         const int ctas = tree_ctas(total, grid);
         // the CTA of unit u is the last one whose first unit is at most u
         c0 = (int)(((u0 + 1) * ctas - 1) / total);

@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(kMgThreads, 1)
         cow = p.refs[shared] - earlier > 1;
         need += cow;
     }
+    need = min(need, p.n_pages + 1);  // more than there are: the sum stays within 32 bits
     int total, n_free, n_cow;
     const int at = block_scan(need, sums, total);
     int have = 0;
@@ -261,25 +262,29 @@ __global__ void __launch_bounds__(kMgThreads, 1)
                 err = kPgBusy;
             else if (len < 0 || len > (long long)p.max_pages * p.page_size)
                 err = kPgCount;
-            else {
+            else
                 held = pages_of(len, p.page_size);
-                p.lengths[b] = len;
-            }
         }
         if (err) pages_fail(p.state, err, i, b);
         s_held[i] = held;
     }
     __syncthreads();
     for (int k = threadIdx.x >> 5; k < n; k += kMgThreads / 32) {
-        const int *from = p.table + (size_t)(s_held[k] < 0 ? 0 : s_src[k]) * p.max_pages;
+        if (s_held[k] < 0) continue;
+        const int *from = p.table + (size_t)s_src[k] * p.max_pages;
+        bool ok = true;
         for (int j = threadIdx.x & 31; j < s_held[k]; j += 32) {
             const int page = from[j];
-            p.table[(size_t)s_dst[k] * p.max_pages + j] = page;
-            if (page >= 0 && page < p.n_pages)
-                atomicAdd(&p.refs[page], 1);
-            else
-                pages_fail(p.state, kPgPosition, k, page);
+            if (page >= 0 && page < p.n_pages) continue;
+            pages_fail(p.state, kPgPosition, k, page);
+            ok = false;
         }
+        if (!__all_sync(0xFFFFFFFFu, ok)) continue;  // a hole in the source's row
+        for (int j = threadIdx.x & 31; j < s_held[k]; j += 32) {
+            p.table[(size_t)s_dst[k] * p.max_pages + j] = from[j];
+            atomicAdd(&p.refs[from[j]], 1);
+        }
+        if ((threadIdx.x & 31) == 0) p.lengths[s_dst[k]] = p.lengths[s_src[k]];
     }
 }
 
