@@ -86,20 +86,20 @@ struct TreeEntry {
 };
 
 // A run of tiles of one item that one CTA works through, and where the walk
-// over the CTA's range of units is; each warp has its own.
+// over the CTA's range of units is (unit `at` of the item, `left` units to
+// go); each warp has its own.
 struct TreeRun {
-    int i, g, rt, t0, t1, tiles, slot, more;
+    int i, g, rt, rts, t0, t1, tiles, slot, more, count, at;
     TreeEntry e;
-    int count;
-    long long u, u1;
+    long long left;
 };
 
 // Shared memory behind the operand tiles.
 struct TreeShared {
     uint64_t full[kTreeMaxStages], empty[kTreeMaxStages];
     uint64_t s_full[2], p_full[2], pv_done[2], q_full, q_empty;
-    TreeRun run[10];       // of each warp
-    float2 ml[2][kTreeM];  // the groups' maxima (scaled) and sums at the end of a run
+    TreeRun first, run[10];  // where the walk begins; of each warp
+    float2 ml[2][kTreeM];    // the groups' maxima (scaled) and sums at the end of a run
     uint32_t tmem;
     int abort, bad_v, pad;
 };
@@ -137,11 +137,19 @@ __device__ __forceinline__ long long tree_before(const TreeArgs &a, const TreeEn
     return sum;
 }
 
-// The units of entry e: tiles of positions x row tiles x KV heads.
+// An item counts kTreeStart units more than it has tiles, in front of them: a
+// run's Q, its first S and its epilogue take as long as some two tiles, so a
+// CTA that goes through several short items gets fewer tiles.
+constexpr int kTreeStart = 2;
+template <int D>
+__device__ __forceinline__ long long tree_start(const TreeArgs &a, const TreeEntry &e, int rt, int rts) {
+    return tree_before<D>(a, e, rt, rts) + (long long)kTreeStart * rt;
+}
+// The units of entry e.
 template <int D>
 __device__ __forceinline__ long long tree_units(const TreeArgs &a, const TreeEntry &e) {
     const int rts = tree_rts<D>(a, e);
-    return e.fresh ? a.p.n_kv_heads * tree_before<D>(a, e, rts, rts) : 0;
+    return e.fresh ? a.p.n_kv_heads * tree_start<D>(a, e, rts, rts) : 0;
 }
 
 // n / d, mostly of small numbers (a 64-bit division takes hundreds of cycles).
@@ -151,36 +159,36 @@ __device__ __forceinline__ long long small_div(long long n, long long d) {
 
 // The warp's next run, false at the end of the CTA's range.
 template <int D>
-__device__ __forceinline__ bool tree_next(const TreeArgs &a, TreeRun &r, const long long *pref, const TreeEntry *ent) {
+__device__ __forceinline__ bool tree_next(const TreeArgs &a, TreeRun &r, const TreeEntry *ent) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) {
-        r.more = r.u < r.u1;
-        if (r.more) {
-            int i = r.i;
-            while (pref[i + 1] <= r.u) ++i;
-            const TreeEntry e = ent[i];
-            r.i = i;
-            r.e = e;
-            const int rts = tree_rts<D>(a, e);
-            const long long head = tree_before<D>(a, e, rts, rts), local = r.u - pref[i];
-            r.g = (int)small_div(local, head);
-            const long long rest = local - r.g * head;
-            int lo = 0, hi = rts;  // the last row tile that starts at or before it
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) / 2;
-                if (tree_before<D>(a, e, mid, rts) <= rest)
-                    lo = mid;
-                else
-                    hi = mid;
+        r.more = 0;
+        while (r.left > 0) {
+            if (r.at == r.tiles + kTreeStart) {  // the next item
+                r.at = 0;
+                if (++r.rt == r.rts) {
+                    r.rt = 0;
+                    if (++r.g == a.p.n_kv_heads) {
+                        r.g = 0;
+                        do
+                            r.e = ent[++r.i];
+                        while (r.e.fresh == 0);
+                        r.rts = tree_rts<D>(a, r.e);
+                    }
+                }
+                r.tiles = tree_tiles<D>(a, r.e, r.rt);
             }
-            r.rt = lo;
-            r.t0 = (int)(rest - tree_before<D>(a, e, lo, rts));
-            r.tiles = tree_tiles<D>(a, e, lo);
-            const long long left = r.u1 - r.u;
-            r.t1 = left < r.tiles - r.t0 ? r.t0 + (int)left : r.tiles;
-            r.slot = 2 * blockIdx.x + (r.count ? 1 : 0);
-            r.count = 1;
-            r.u += r.t1 - r.t0;
+            const int to = (int)min((long long)(r.tiles + kTreeStart), r.at + r.left);
+            r.t0 = max(r.at - kTreeStart, 0);
+            r.t1 = max(to - kTreeStart, 0);
+            r.left -= to - r.at;
+            r.at = to;
+            if (r.t0 < r.t1) {
+                r.slot = 2 * blockIdx.x + (r.count ? 1 : 0);
+                r.count = 1;
+                r.more = 1;
+                break;
+            }
         }
     }
     __syncwarp();
@@ -360,7 +368,7 @@ struct TreeOut {
     float inv;                 // 1 / sum for the result, 1 for a record
     float m2, bias;
     int c0, c1, g, t;
-    bool mine, other, live, whole, ok;
+    bool join, mine, other, live, whole, ok;  // join: both groups' O go into a row
     float4 *rec;
     uint16_t *to;
 };
@@ -371,18 +379,24 @@ struct TreeOut {
 template <int D, bool BF16, bool ADD>
 __device__ __forceinline__ void tree_write(const TreeArgs &a, const TreeRun &r, const TreeOut w) {
 #pragma unroll 1
-    for (int c = w.c0; c < w.c1; c += 16) {
-        float o[16], x[16];
-        tmem_ld16n(w.o_mine + c, o);
-        tmem_ld16n(w.o_other + c, x);
-        tmem_wait_ld16(o);
-        tmem_wait_ld16(x);
+    for (int c = w.c0; c < w.c1; c += 32) {
+        float o[32];
+        tmem_ld32(w.o_mine + c, o);
+        if (w.join) {
+            float x[32];
+            tmem_ld32(w.o_other + c, x);
+            tmem_wait_ld(o);
+            tmem_wait_ld(x);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {  // an O that no tile went into is not used
-            o[k] = w.mine ? o[k] * w.f0 : 0.f;
-            o[k] = w.other ? fmaf(x[k], w.f1, o[k]) : o[k];
-            o[k] = w.ok ? o[k] : CUDART_NAN_F;
+            for (int k = 0; k < 32; ++k) {  // an O that no tile went into is not used
+                o[k] = w.mine ? o[k] * w.f0 : 0.f;
+                o[k] = w.other ? fmaf(x[k], w.f1, o[k]) : o[k];
+            }
+        } else {
+            tmem_wait_ld(o);
         }
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] = w.ok ? o[k] : CUDART_NAN_F;
         if (w.live) {
             if constexpr (ADD) {
                 const uint16_t *q = a.q + ((size_t)r.i * a.T + w.t) * a.q_stride + (size_t)(r.g * a.G + w.g) * D;
@@ -402,12 +416,12 @@ __device__ __forceinline__ void tree_write(const TreeArgs &a, const TreeRun &r, 
                     for (int k = 0; k < D; ++k) dot = fmaf(from16<BF16>(q[k]), from16<BF16>(a.k[at + k]), dot);
                     const float p = ex2(fmaf(dot, a.scale, w.bias - (w.m2 == -CUDART_INF_F ? 0.f : w.m2)));
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) o[k] = fmaf(p, from16<BF16>(a.v[at + c + k]), o[k]);
+                    for (int k = 0; k < 32; ++k) o[k] = fmaf(p, from16<BF16>(a.v[at + c + k]), o[k]);
                 }
             }
             if (w.whole) {
 #pragma unroll
-                for (int k = 0; k < 16; k += 8) {
+                for (int k = 0; k < 32; k += 8) {
                     uint4 v;
                     v.x = pack16<BF16>(o[k] * w.inv, o[k + 1] * w.inv);
                     v.y = pack16<BF16>(o[k + 2] * w.inv, o[k + 3] * w.inv);
@@ -418,7 +432,7 @@ __device__ __forceinline__ void tree_write(const TreeArgs &a, const TreeRun &r, 
             } else {
                 float4 *rec = w.rec + (size_t)(c / 4) * a.rows_cap;
 #pragma unroll
-                for (int k = 0; k < 16; k += 4)
+                for (int k = 0; k < 32; k += 4)
                     rec[(size_t)(k / 4) * a.rows_cap] = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
             }
         }
@@ -497,29 +511,50 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
             if (base + lane < a.n) pref[base + lane + 1] = carry + x;
             carry += __shfl_sync(0xFFFFFFFFu, x, 31);
         }
-        if (lane == 0) pref[0] = 0;
+        __syncwarp();
+        if (lane == 0) {  // where this CTA begins
+            TreeRun &r = sh.first;
+            const long long U = carry;
+            const int ctas = tree_ctas(U, gridDim.x);
+            const bool mine = (int)blockIdx.x < ctas;
+            const long long u = mine ? tree_first(U, ctas, blockIdx.x) : 0;
+            r.left = mine ? tree_first(U, ctas, blockIdx.x + 1) - u : 0;
+            r.count = 0;
+            pref[0] = 0;
+            if (r.left) {
+                int lo = 0, hi = a.n;  // the last entry that starts at or before u
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) / 2;
+                    if (pref[mid] <= u)
+                        lo = mid;
+                    else
+                        hi = mid;
+                }
+                r.i = lo;
+                r.e = ent[lo];
+                r.rts = tree_rts<D>(a, r.e);
+                const long long head = tree_start<D>(a, r.e, r.rts, r.rts), local = u - pref[lo];
+                r.g = (int)small_div(local, head);
+                const long long rest = local - r.g * head;
+                lo = 0, hi = r.rts;  // the last row tile that starts at or before it
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) / 2;
+                    if (tree_start<D>(a, r.e, mid, r.rts) <= rest)
+                        lo = mid;
+                    else
+                        hi = mid;
+                }
+                r.rt = lo;
+                r.at = (int)(rest - tree_start<D>(a, r.e, lo, r.rts));
+                r.tiles = tree_tiles<D>(a, r.e, lo);
+            }
+        }
     }
     __syncthreads();
     pdl_launch_dependents();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&sh.tmem);
     TreeRun &run = sh.run[warp];
-    if (lane == 0) {
-        const long long U = pref[a.n];
-        const int ctas = tree_ctas(U, gridDim.x);
-        const bool mine = (int)blockIdx.x < ctas;
-        run.u = mine ? tree_first(U, ctas, blockIdx.x) : 0;
-        run.u1 = mine ? tree_first(U, ctas, blockIdx.x + 1) : 0;
-        int lo = 0, hi = a.n;  // the last entry that starts at or before u
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (pref[mid] <= run.u)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        run.i = lo;
-        run.count = 0;
-    }
+    if (lane == 0) run = sh.first;
     int issued = 0, q_issued = 0;  // the loader's ring loads and runs whose Q it loaded
     // Jobs of a run, in order: with two row tiles (both groups on every tile)
     // job j is group j & 1 of tile j / 2, else S buffer j & 1 of tile j.
@@ -536,7 +571,7 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
         int slot = 0, seg_no = 0;
         uint32_t phase = 1;  // of empty[slot]: the first round waits for nothing
         bool ok = true;
-        while (ok && tree_next<D>(a, run, pref, ent)) {
+        while (ok && tree_next<D>(a, run, ent)) {
             const int *row = a.p.table + (size_t)run.e.seq * a.p.max_pages;
             const int end = run.e.len + run.e.fresh, t0 = run.t0, t1 = run.t1, g = run.g;
             const bool mine = lane < ns * nh;
@@ -611,7 +646,7 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
         };
         // The whole warp runs the loop (its values stay uniform, as the MMA's
         // operands have to be); one elected lane issues.
-        while (ok && tree_next<D>(a, run, pref, ent)) {
+        while (ok && tree_next<D>(a, run, ent)) {
             const int nt = __shfl_sync(0xFFFFFFFFu, run.t1 - run.t0, 0);
             const bool two = __shfl_sync(0xFFFFFFFFu, (int)two_rows(), 0);
             const int jobs = two ? 2 * nt : nt;
@@ -677,7 +712,7 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
         uint32_t seen[2] = {0, 0}, done = 0;  // S of each buffer taken, P V waited for
         bool ok = true;
         const int my_tok = gt / a.G, my_g = gt - my_tok * a.G;
-        while (tree_next<D>(a, run, pref, ent)) {
+        while (tree_next<D>(a, run, ent)) {
             const int nt = run.t1 - run.t0;
             const bool two = two_rows(), join = NG == 2 && !two;
             const int tok0 = run.rt * NG * a.toks + (two ? grp * a.toks : 0);  // first token of this row tile
@@ -835,6 +870,7 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
             }
             tc_fence_after();
             w.ok = ok;
+            w.join = join;
             w.live = live;
             w.whole = run.t0 == 0 && run.t1 == run.tiles;
             w.m2 = m * a.scale;
@@ -891,19 +927,27 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
 }
 
 // Joins the records of every item that more than one CTA worked on: CTA
-// (x, i, g) 8 R rows of an item of KV head g of entry i, a thread 4 columns of
-// R rows (8 rows of a column block are side by side in a record).  R = 4 where
-// that leaves CTAs enough: a CTA takes some 3 us whatever it finds to join.
-constexpr int kCombineThreads = 256;
+// (x, i, g) 8 R rows and up to 128 columns of an item of KV head g of entry i,
+// a thread 4 columns of R rows (8 rows of a column block are side by side in a
+// record).  The time is that of one round of loads after another, so the first
+// 16 of a thread go out before the weights are known.  R = 4 where that leaves
+// CTAs enough: a CTA takes some 3 us whatever it finds to join.
+template <int D>
+struct Combine {
+    static constexpr int kCols = D < 128 ? D : 128, kThreads = 2 * kCols, kWarps = kThreads / 32;
+};
 
 template <int D, bool BF16, int R>
-__global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const __grid_constant__ TreeArgs a, int grid) {
-    constexpr int NG = tree_groups(D), kCombineRows = 8 * R;
-    __shared__ long long s_red[2][kCombineThreads / 32];
+__global__ void __launch_bounds__(Combine<D>::kThreads) tree_combine_kernel(const __grid_constant__ TreeArgs a, int grid) {
+    constexpr int NG = tree_groups(D), kCombineRows = 8 * R, kCols = Combine<D>::kCols;
+    constexpr int kCombineThreads = Combine<D>::kThreads, kWarps = Combine<D>::kWarps;
+    constexpr int kBatch = 16 / R;  // records whose loads a thread has in flight
+    __shared__ long long s_red[2][kWarps];
     __shared__ float s_w[kTreeMaxCtas][kCombineRows];  // weight of each record's row
     __shared__ float s_inv[kCombineRows];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int i = blockIdx.y, g = blockIdx.z, blocks = (a.rows_cap + kCombineRows - 1) / kCombineRows;
+    const int i = blockIdx.y, g = blockIdx.z / (D / kCols), c4 = blockIdx.z % (D / kCols) * (kCols / 4) + warp * 4 + (lane >> 3);
+    const int blocks = (a.rows_cap + kCombineRows - 1) / kCombineRows;
     const int rt = blockIdx.x / blocks, r0 = (blockIdx.x - rt * blocks) * kCombineRows;
     // units before entry i, and of all entries
     long long before = 0, total = 0;
@@ -926,7 +970,7 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const __g
     __syncthreads();
     before = total = 0;
 #pragma unroll
-    for (int k = 0; k < kCombineThreads / 32; ++k) {
+    for (int k = 0; k < kWarps; ++k) {
         before += s_red[0][k];
         total += s_red[1][k];
     }
@@ -934,23 +978,34 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const __g
     const int rts = tree_rts<D>(a, te);
     int c0 = 0, c1 = 0, slot0 = 0;
     if (rt < rts) {
-        const long long u0 = before + g * tree_before<D>(a, te, rts, rts) + tree_before<D>(a, te, rt, rts);
-        const long long u1 = u0 + tree_tiles<D>(a, te, rt);
+        const long long start = before + g * tree_start<D>(a, te, rts, rts) + tree_start<D>(a, te, rt, rts);
+        const long long u0 = start + kTreeStart, u1 = u0 + tree_tiles<D>(a, te, rt);
         const int ctas = tree_ctas(total, grid);
         // the CTA of unit u is the last one whose first unit is at most u
         c0 = (int)(((u0 + 1) * ctas - 1) / total);
         c1 = (int)((u1 * ctas - 1) / total);
         // of these CTAs only the first one's record can be its second
-        slot0 = 2 * c0 + (tree_first(total, ctas, c0) < u0 ? 1 : 0);
+        slot0 = 2 * c0 + (tree_first(total, ctas, c0) < start ? 1 : 0);
     }
     const int count = c1 - c0 + 1;
     pdl_wait();              // the records are complete
     if (c0 == c1) return;    // none, or the item's only CTA wrote the result
     auto slot = [&](int c) { return (size_t)(c == 0 ? slot0 : 2 * (c0 + c)); };
-    // a warp takes R rows, 32 / R lanes each: maximum, weights and sum
-    {
-        constexpr int kL = 32 / R;
-        const int x = warp * R + lane / kL, c_first = lane % kL;
+    const size_t pitch = (size_t)(D / 4) * a.rows_cap;
+    const float4 *rec = a.part_o + (size_t)c4 * a.rows_cap + r0 + (lane & 7);
+    float4 v[kBatch][R];
+    auto load = [&](int first) {
+#pragma unroll
+        for (int c = 0; c < kBatch; ++c)
+#pragma unroll
+            for (int x = 0; x < R; ++x)
+                if (first + c < count && r0 + 8 * x + (lane & 7) < a.rows_cap)
+                    v[c][x] = rec[slot(first + c) * pitch + 8 * x];
+    };
+    load(0);
+    {  // kL lanes a row: maximum, weights and sum
+        constexpr int kL = kCombineThreads / kCombineRows;
+        const int x = threadIdx.x / kL, c_first = threadIdx.x % kL;
         const bool real = r0 + x < a.rows_cap;
         float M = -CUDART_INF_F, L = 0.f;
         for (int c = c_first; real && c < count; c += kL) M = fmaxf(M, a.part_ml[slot(c) * a.rows_cap + r0 + x].x);
@@ -968,25 +1023,24 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const __g
         if (c_first == 0) s_inv[x] = L == 0.f ? 0.f : 1.f / L;
     }
     __syncthreads();
-    const size_t pitch = (size_t)(D / 4) * a.rows_cap;
-    for (int c4 = warp * 4 + (lane >> 3); c4 < D / 4; c4 += kCombineThreads / 8) {
-        const float4 *rec = a.part_o + (size_t)c4 * a.rows_cap + r0 + (lane & 7);
+    {
         float4 o[R];
 #pragma unroll
         for (int x = 0; x < R; ++x) o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll(R == 1 ? 8 : 2)
-        for (int c = 0; c < count; ++c) {
-            const float4 *at = rec + slot(c) * pitch;
+#pragma unroll 1
+        for (int first = 0; first < count; first += kBatch) {
+            if (first) load(first);
 #pragma unroll
-            for (int x = 0; x < R; ++x) {
-                if (r0 + 8 * x + (lane & 7) >= a.rows_cap) continue;
-                const float4 v = at[8 * x];
-                const float f = s_w[c][8 * x + (lane & 7)];
-                o[x].x = fmaf(f, v.x, o[x].x);
-                o[x].y = fmaf(f, v.y, o[x].y);
-                o[x].z = fmaf(f, v.z, o[x].z);
-                o[x].w = fmaf(f, v.w, o[x].w);
-            }
+            for (int c = 0; c < kBatch; ++c)
+#pragma unroll
+                for (int x = 0; x < R; ++x) {
+                    if (first + c >= count || r0 + 8 * x + (lane & 7) >= a.rows_cap) continue;
+                    const float f = s_w[first + c][8 * x + (lane & 7)];
+                    o[x].x = fmaf(f, v[c][x].x, o[x].x);
+                    o[x].y = fmaf(f, v[c][x].y, o[x].y);
+                    o[x].z = fmaf(f, v[c][x].z, o[x].z);
+                    o[x].w = fmaf(f, v[c][x].w, o[x].w);
+                }
         }
 #pragma unroll
         for (int x = 0; x < R; ++x) {
@@ -1034,10 +1088,12 @@ static cudaError_t launch_tree(const CUtensorMap &mq, const CUtensorMap &mk, con
     // 8 rows a CTA, or 32 once 8 make more CTAs than run at the same time
     const int item = tree_groups(D) * a.toks, rts = (a.T + item - 1) / item;
     const auto blocks = [&](int rows) { return (a.rows_cap + rows - 1) / rows; };
-    const bool few = (long long)rts * blocks(8) * a.n * a.p.n_kv_heads <= 6LL * grid;
+    constexpr int col_blocks = D / Combine<D>::kCols;
+    const bool few = (long long)rts * blocks(8) * a.n * a.p.n_kv_heads * col_blocks <= 6LL * grid;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(rts * blocks(few ? 8 : 32)), (unsigned)a.n, (unsigned)a.p.n_kv_heads);
-    cfg.blockDim = dim3(kCombineThreads);
+    cfg.gridDim = dim3((unsigned)(rts * blocks(few ? 8 : 32)), (unsigned)a.n,
+                       (unsigned)(a.p.n_kv_heads * col_blocks));
+    cfg.blockDim = dim3(Combine<D>::kThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
