@@ -25,12 +25,14 @@ _TYPES = {torch.bfloat16: MK_BF16, torch.float16: MK_FP16, torch.float32: MK_FP3
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream().cuda_stream without its 2 us
+_get_device = torch._C._cuda_getDevice  # current_device() without its check of the initialisation
+_INT32 = torch.int32
 
 
 def _elsewhere(device: torch.device, stream) -> bool:
     """Does a call have to switch to another device or stream first?"""
     if stream is None:
-        return torch.cuda.current_device() != device.index
+        return _get_device() != device.index
     if stream.device != device:
         raise ValueError(f"the stream must be one of {device}")
     return True
@@ -41,12 +43,12 @@ def _on(device: torch.device, stream):
     return torch.cuda.stream(torch.cuda.current_stream(device) if stream is None else stream)
 
 
-def _ints(t, name: str, shape: tuple, device: torch.device):
-    """The address of an int32 list of that shape (None stays None)."""
+def _ints(t, name: str, shape: tuple, index: int):
+    """The address of an int32 list of that shape on CUDA device `index` (None stays None)."""
     if t is None:
         return None
-    if t.dtype is not torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {device}")
+    if t.dtype is not _INT32 or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on cuda:{index}")
     return t.data_ptr()
 
 
@@ -95,9 +97,10 @@ class PagedCache:
             raise ValueError("table must be [max_seqs, max_pages]")
         self.max_seqs, self.max_pages = table.shape
         self.device, self.dtype = kv.device, kv.dtype
-        _ints(table, "table", (self.max_seqs, self.max_pages), kv.device)
-        _ints(lengths, "lengths", (self.max_seqs,), kv.device)
-        _ints(refs, "refs", (self.n_pages,), kv.device)
+        self._index = kv.device.index
+        _ints(table, "table", (self.max_seqs, self.max_pages), self._index)
+        _ints(lengths, "lengths", (self.max_seqs,), self._index)
+        _ints(refs, "refs", (self.n_pages,), self._index)
         self.kv, self.table, self.lengths, self.refs = kv, table, lengths, refs
         self.lib = load()
         self._state = torch.zeros(self.lib.mk_pages_state_bytes() // 4, dtype=torch.int32, device=kv.device)
@@ -112,7 +115,7 @@ class PagedCache:
         if _elsewhere(self.device, stream):
             with _on(self.device, stream):
                 return self._call(name, None, *args)
-        st = getattr(self.lib, name)(self._ref, *args, _raw_stream(self.device.index))
+        st = getattr(self.lib, name)(self._ref, *args, _raw_stream(self._index))
         if st:
             check(st, None, name, op=True)
 
@@ -125,7 +128,7 @@ class PagedCache:
         return need
 
     def _list(self, name: str, t: torch.Tensor, n: int) -> int:
-        return _ints(t, name, (n,), self.device)
+        return _ints(t, name, (n,), self._index)
 
     def reserve(self, seqs: torch.Tensor, counts: torch.Tensor, stream=None) -> None:
         """Room for counts[i] new tokens of sequence seqs[i], in pages it holds alone."""
@@ -143,7 +146,7 @@ class PagedCache:
         n = seqs.numel()
         width = 0 if keep is None else keep.shape[-1]
         self._call("mk_pages_compact", stream, self._list("seqs", seqs, n), self._list("n_keep", n_keep, n),
-                   _ints(keep, "keep", (n, width), self.device), width, n)
+                   _ints(keep, "keep", (n, width), self._index), width, n)
 
     def free(self, seqs: torch.Tensor, lengths: torch.Tensor | None = None, stream=None) -> None:
         """Cut sequence seqs[i] to lengths[i] positions (0 by default) and give up the pages behind."""
@@ -185,14 +188,14 @@ def tree_mask(parents: torch.Tensor) -> torch.Tensor:
     return torch.where(packed >= 1 << 31, packed - (1 << 32), packed).to(torch.int32)
 
 
-def _tokens(x: torch.Tensor, name: str, shape: tuple, dtypes, device: torch.device) -> int:
-    """Checks a [n, T, ...] tensor whose tokens are dense rows at one stride;
-    returns that stride in elements."""
+def _tokens(x: torch.Tensor, name: str, shape: tuple, dtypes, index: int, width: int) -> int:
+    """Checks a [n, T, ...] tensor whose tokens are dense rows of `width` values
+    at one stride; returns that stride in elements."""
+    if x.shape != shape or x.dtype not in dtypes or x.get_device() != index:
+        raise ValueError(f"{name} must be {list(shape)} of {' or '.join(str(t) for t in dtypes)} on cuda:{index}")
+    if x.is_contiguous():
+        return width
     n, T = shape[:2]
-    if x.shape != shape or x.dtype not in dtypes or x.device != device:
-        raise ValueError(f"{name} must be {list(shape)} of {' or '.join(str(t) for t in dtypes)} on {device}")
-    if x.is_contiguous() and n * T:
-        return x.numel() // (n * T)
     width = 1
     for k in range(x.dim() - 1, 1, -1):
         if x.shape[k] != 1 and x.stride(k) != width:
@@ -216,11 +219,13 @@ def qk_norm_rope(qkv: torch.Tensor, cache: PagedCache, layer: int, seqs: torch.T
     are left out."""
     if qkv.dim() != 3:
         raise ValueError("qkv must be [n, T, (n_heads + 2 n_kv_heads) * head_dim]")
-    n, T = qkv.shape[:2]
-    d, dev = cache.head_dim, cache.device
-    stride = _tokens(qkv, "qkv", (n, T, (n_heads + 2 * cache.n_kv_heads) * d), (torch.float32, cache.dtype), dev)
+    n, T, _ = qkv.shape
+    d, dev, at = cache.head_dim, cache.device, cache._index
+    width = (n_heads + 2 * cache.n_kv_heads) * d
+    stride = _tokens(qkv, "qkv", (n, T, width), (torch.float32, cache.dtype), at, width)
     for g in (q_gain, k_gain):
-        if g is not None and (g.dtype != torch.bfloat16 or g.shape != (d,) or g.device != dev or not g.is_contiguous()):
+        if g is not None and (g.dtype is not torch.bfloat16 or g.shape != (d,) or g.get_device() != at
+                              or not g.is_contiguous()):
             raise ValueError("gains must be contiguous bf16 [head_dim]")
     if _elsewhere(dev, stream):
         with _on(dev, stream):
@@ -228,10 +233,10 @@ def qk_norm_rope(qkv: torch.Tensor, cache: PagedCache, layer: int, seqs: torch.T
     if out is None:
         out = torch.empty((n, T, n_heads, d), dtype=cache.dtype, device=dev)
     st = cache.lib.mk_qk_norm_rope(
-        cache._ref, layer, qkv.data_ptr(), _TYPES[qkv.dtype], stride, n, T, n_heads, _ints(seqs, "seqs", (n,), dev),
-        _ints(n_new, "n_new", (n,), dev), _ints(depth, "depth", (n, T), dev),
+        cache._ref, layer, qkv.data_ptr(), _TYPES[qkv.dtype], stride, n, T, n_heads, _ints(seqs, "seqs", (n,), at),
+        _ints(n_new, "n_new", (n,), at), _ints(depth, "depth", (n, T), at),
         None if q_gain is None else q_gain.data_ptr(), None if k_gain is None else k_gain.data_ptr(), eps, theta,
-        out.data_ptr(), _tokens(out, "out", (n, T, n_heads, d), (cache.dtype,), dev), _raw_stream(dev.index))
+        out.data_ptr(), _tokens(out, "out", (n, T, n_heads, d), (cache.dtype,), at, n_heads * d), _raw_stream(at))
     if st:
         check(st, None, "mk_qk_norm_rope", op=True)
     return out
@@ -250,9 +255,9 @@ def attention_tree(q: torch.Tensor, cache: PagedCache, layer: int, seqs: torch.T
     if q.dim() != 4:
         raise ValueError("q must be [n, T, n_heads, head_dim]")
     n, T, nq, d = q.shape
-    dev = cache.device
-    shape = (n, T, nq, cache.head_dim)
-    stride = _tokens(q, "q", shape, (cache.dtype,), dev)
+    dev, at = cache.device, cache._index
+    shape, types = (n, T, nq, cache.head_dim), (cache.dtype,)
+    stride = _tokens(q, "q", shape, types, at, nq * d)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return attention_tree(q, cache, layer, seqs, n_new, mask, out, scratch)
@@ -261,14 +266,13 @@ def attention_tree(q: torch.Tensor, cache: PagedCache, layer: int, seqs: torch.T
     elif out.data_ptr() == q.data_ptr():
         raise ValueError("out must not be q")
     if scratch is None:
-        scratch = torch.empty(cache._scratch_bytes(T, nq), dtype=torch.uint8, device=dev)
-    elif scratch.device != dev or not scratch.is_contiguous():
+        scratch = cache._state.new_empty(cache._scratch_bytes(T, nq) // 4)
+    elif scratch.get_device() != at or not scratch.is_contiguous():
         raise ValueError("scratch must be a contiguous tensor on the cache's device")
     st = cache.lib.mk_attention_tree(
-        cache._ref, layer, q.data_ptr(), stride, n, T, nq, _ints(seqs, "seqs", (n,), dev),
-        _ints(n_new, "n_new", (n,), dev), _ints(mask, "mask", (n, T, (T + 31) // 32), dev), out.data_ptr(),
-        _tokens(out, "out", shape, (cache.dtype,), dev), scratch.data_ptr(),
-        scratch.numel() * scratch.element_size(), _raw_stream(dev.index))
+        cache._ref, layer, q.data_ptr(), stride, n, T, nq, _ints(seqs, "seqs", (n,), at),
+        _ints(n_new, "n_new", (n,), at), _ints(mask, "mask", (n, T, (T + 31) // 32), at), out.data_ptr(),
+        _tokens(out, "out", shape, types, at, nq * d), scratch.data_ptr(), scratch.nbytes, _raw_stream(at))
     if st:
         check(st, None, "mk_attention_tree", op=True)
     return out
