@@ -440,3 +440,36 @@ def test_projection_to_attention_to_projection():
     exact = o.cpu().double().view(n * T, -1) @ wo.double().T
     slack = 2 * nq * d * 2.0 ** -24 * (o.cpu().double().view(n * T, -1).abs() @ wo.double().abs().T)
     assert ((y.cpu().double() - exact).abs() <= slack + 2.0 ** -23 * exact.abs()).all()
+
+
+def test_offsets_behind_32_bits():
+    """The same sequences in a small pool and at the end of one of more than
+    2^32 values: the same bits."""
+    import tile_synchronised_b200 as mk
+    nkv, ps, d, nq, T = 8, 64, 128, 16, 5
+    small = filled([130, 64, 7], [64, 64, 64], layers=1, nkv=nkv, d=d, ps=ps, seed=21, poison=False)
+    a = small.to_cache()
+    n = a.n_pages
+    pages = 33100
+    kv = torch.empty((2, 1, pages, nkv, ps, d), dtype=torch.bfloat16, device="cuda")
+    assert kv.numel() // 2 > 2 ** 31 and kv.numel() > 2 ** 32
+    kv[:, :, pages - n:] = a.kv
+    refs = torch.ones(pages, dtype=torch.int32, device="cuda")
+    refs[pages - n:] = a.refs
+    b = mk.PagedCache.over(kv, torch.where(a.table >= 0, a.table + (pages - n), -1), a.lengths.clone(), refs)
+    seqs = ints(2, 0, 1)
+    qkv = torch.randn((3, T, (nq + 2 * nkv) * d), generator=generator(4)).cuda()
+    mask = pack_bits(torch.stack([visible(random_tree(T, k)) for k in range(3)])).cuda()
+    got = []
+    for c in (a, b):
+        q = mk.qk_norm_rope(qkv, c, 0, seqs, nq, 10000.0)
+        o = mk.attention_tree(q, c, 0, seqs, mask=mask)
+        c.compact(seqs, ints(3, 2, 1), torch.tensor([[0, 2, 4], [1, 3, 0], [4, 0, 0]], dtype=torch.int32).cuda())
+        c.check()
+        got.append((q, o, c.lengths, c.kv[:, :, c.n_pages - n:]))
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+    src, dst = ints(pages - n, pages - 1), ints(0, 1)
+    b.copy(src, dst)
+    b.check()
+    assert torch.equal(kv[:, :, 0], kv[:, :, pages - n]) and torch.equal(kv[:, :, 1], kv[:, :, pages - 1])

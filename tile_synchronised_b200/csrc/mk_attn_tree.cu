@@ -41,6 +41,13 @@
 // at a time, ahead); one lane issues the MMAs: with two jobs (tile, group) in
 // flight, S of job j + 2 follows P V of job j.
 //
+// Measured (graph replays): single tokens of 16 sequences to 16k 102 us (5.9
+// TB/s, 0.90 of the measured copy), 64 drafts of 16 sequences at 8k to 16k 216
+// to 235 us (exponentials and MMAs 2048 cycles each per tile of 256 rows, the
+// chain through both some 4000), 8 trees of 27 28 to 30 us, d = 256 trees 20 us,
+// chunks of 500 tokens 31 to 35 us, one small tree 12 us: of the last four
+// some 6 us pass before the first S and some 8 after the last P V.
+//
 // P is rounded to the cache's 16-bit type (2^-8 relative at most in bf16, each
 // element on its own, as V's own storage); S, the maximum, the sum, O and the
 // records are 32 bits.
@@ -565,7 +572,7 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
         const int seg = a.seg, ns = NT / seg, per = 32 / ns;
         const int nh = ns > 1 ? NH : 1;  // a whole tile's box covers every 64-column block
         const int my = lane / nh, blk = lane - my * nh;
-        const int nkv = a.p.n_kv_heads, ps = a.p.page_size;
+        const int nkv = a.p.n_kv_heads, ps = a.p.page_size, off_step = NT % ps, seg_log = 31 - __clz(seg);
         const uint32_t seg_bytes = (uint32_t)seg * D * 2, off_smem = (uint32_t)(blk * NT + my * seg) * 128u;
         const uint32_t q_bytes = (uint32_t)(a.toks * a.G) * D * 2;
         int slot = 0, seg_no = 0;
@@ -595,6 +602,7 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
                 return true;
             };
             int tb = t0, pages = look(tb), next = look(tb + per);
+            int off = (t0 * NT + my * seg) % ps;  // of this lane's part in its page
             if (seg_no == 0) ok = load_q();
             for (int t = t0; ok && t < t1; ++t) {
                 if (t - tb == per) {
@@ -603,13 +611,13 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
                     next = look(tb + per);
                 }
                 int page = __shfl_sync(0xFFFFFFFFu, pages, ((t - tb) * ns + my) & 31);
-                const int pos = t * NT + my * seg, off = pos - pos / ps * ps;
+                const int pos = t * NT + my * seg;
                 const bool go = mine && pos < end;
                 if (go && (page < 0 || page >= a.p.n_pages)) {
                     pages_fail(a.p.state, kPgPosition, run.i, pos);
                     page = -1;  // out of the tensor: zeros
                 }
-                const int head = page < 0 ? -1 : page * nkv + g, left = (end - t * NT + seg - 1) / seg;
+                const int head = page < 0 ? -1 : page * nkv + g, left = (end - t * NT + seg - 1) >> seg_log;
                 const uint32_t bytes = (uint32_t)(left < ns ? left : ns) * seg_bytes;
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv) {
@@ -623,6 +631,8 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
                     ++issued;
                     if (++slot == S) slot = 0, phase ^= 1u;
                 }
+                off += off_step;
+                if (off >= ps) off -= ps;
                 // the last Q is free once its last S is done; this run's first tile does not wait for that
                 if (t == t0 && seg_no) ok = ok && __all_sync(0xFFFFFFFFu, load_q());
             }
@@ -713,20 +723,21 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
         bool ok = true;
         const int my_tok = gt / a.G, my_g = gt - my_tok * a.G;
         while (tree_next<D>(a, run, ent)) {
-            const int nt = run.t1 - run.t0;
+            const int nt = run.t1 - run.t0, t0 = run.t0, entry = run.i;
+            const TreeEntry e = run.e;
             const bool two = two_rows(), join = NG == 2 && !two;
             const int tok0 = run.rt * NG * a.toks + (two ? grp * a.toks : 0);  // first token of this row tile
-            const int rows = min(a.toks, run.e.fresh - tok0) * a.G, t = tok0 + my_tok;
+            const int rows = min(a.toks, e.fresh - tok0) * a.G, t = tok0 + my_tok;
             const bool live = gt < rows, warp_live = gw * 32 < rows;
             float m = -CUDART_INF_F, l = 0.f;  // the maximum that P and the sum refer to (of S unscaled)
             const int step = join ? 2 : 1, first = join ? grp : 0;
             for (int i = first; i < nt; i += step) {
-                const int b = NG == 2 ? grp : i & 1, p0 = (run.t0 + i) * NT;
+                const int b = NG == 2 ? grp : i & 1, p0 = (t0 + i) * NT;
                 const uint32_t sc = lanes + (uint32_t)b * 128;
-                const bool tail = p0 + NT > run.e.len;  // new tokens, or nothing, in this tile
+                const bool tail = p0 + NT > e.len;  // new tokens, or nothing, in this tile
                 uint32_t bits[NT / 32];
                 if (tail) {
-                    tree_bits<NT / 32>(a, run.i, live ? t : 0, run.e, p0, bits);
+                    tree_bits<NT / 32>(a, entry, live ? t : 0, e, p0, bits);
 #pragma unroll
                     for (int c = 0; c < NT / 32; ++c) bits[c] = live ? bits[c] : 0u;
                 }
@@ -834,12 +845,12 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     const int pos = p0 + gt;
-                    if (gt < NT && pos >= run.e.len) {
+                    if (gt < NT && pos >= e.len) {
                         uint8_t *vr = ring + (size_t)st * kStage + gt * 128;
                         auto chunk = [&](int c) {  // 16-byte chunk c of the row
                             return reinterpret_cast<uint4 *>(vr + (c / 8) * NT * 128 + (((c & 7) ^ (gt & 7)) << 4));
                         };
-                        bool clear = pos >= run.e.len + run.e.fresh;
+                        bool clear = pos >= e.len + e.fresh;
                         if (!clear) {
 #pragma unroll 8
                             for (int c = 0; c < D / 8; ++c) clear |= any_nonfinite<BF16>(*chunk(c));
@@ -989,30 +1000,36 @@ __global__ void __launch_bounds__(Combine<D>::kThreads) tree_combine_kernel(cons
     }
     const int count = c1 - c0 + 1;
     pdl_wait();              // the records are complete
-    if (c0 == c1) return;    // none, or the item's only CTA wrote the result
+    // none, or the item's only CTA wrote the result; or rows of no token
+    const auto token = [&](int r) { return (rt * NG + r / kTreeM) * a.toks + (r & (kTreeM - 1)) / a.G; };
+    const auto real = [&](int r) { return r < a.rows_cap && (r & (kTreeM - 1)) < a.toks * a.G && token(r) < e.fresh; };
+    if (c0 == c1 || !real(r0)) return;
     auto slot = [&](int c) { return (size_t)(c == 0 ? slot0 : 2 * (c0 + c)); };
     const size_t pitch = (size_t)(D / 4) * a.rows_cap;
     const float4 *rec = a.part_o + (size_t)c4 * a.rows_cap + r0 + (lane & 7);
     float4 v[kBatch][R];
+    bool live[R];
+#pragma unroll
+    for (int x = 0; x < R; ++x) live[x] = real(r0 + 8 * x + (lane & 7));
     auto load = [&](int first) {
 #pragma unroll
         for (int c = 0; c < kBatch; ++c)
 #pragma unroll
             for (int x = 0; x < R; ++x)
-                if (first + c < count && r0 + 8 * x + (lane & 7) < a.rows_cap)
+                if (first + c < count && live[x])
                     v[c][x] = rec[slot(first + c) * pitch + 8 * x];
     };
     load(0);
     {  // kL lanes a row: maximum, weights and sum
         constexpr int kL = kCombineThreads / kCombineRows;
         const int x = threadIdx.x / kL, c_first = threadIdx.x % kL;
-        const bool real = r0 + x < a.rows_cap;
+        const bool mine = real(r0 + x);
         float M = -CUDART_INF_F, L = 0.f;
-        for (int c = c_first; real && c < count; c += kL) M = fmaxf(M, a.part_ml[slot(c) * a.rows_cap + r0 + x].x);
+        for (int c = c_first; mine && c < count; c += kL) M = fmaxf(M, a.part_ml[slot(c) * a.rows_cap + r0 + x].x);
 #pragma unroll
         for (int o = kL / 2; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
         if (M == -CUDART_INF_F) M = 0.f;
-        for (int c = c_first; real && c < count; c += kL) {
+        for (int c = c_first; mine && c < count; c += kL) {
             const float2 ml = a.part_ml[slot(c) * a.rows_cap + r0 + x];
             const float f = ex2(ml.x - M);
             s_w[c][x] = f;
@@ -1034,7 +1051,7 @@ __global__ void __launch_bounds__(Combine<D>::kThreads) tree_combine_kernel(cons
             for (int c = 0; c < kBatch; ++c)
 #pragma unroll
                 for (int x = 0; x < R; ++x) {
-                    if (first + c >= count || r0 + 8 * x + (lane & 7) >= a.rows_cap) continue;
+                    if (first + c >= count || !live[x]) continue;
                     const float f = s_w[first + c][8 * x + (lane & 7)];
                     o[x].x = fmaf(f, v[c][x].x, o[x].x);
                     o[x].y = fmaf(f, v[c][x].y, o[x].y);
@@ -1044,8 +1061,8 @@ __global__ void __launch_bounds__(Combine<D>::kThreads) tree_combine_kernel(cons
         }
 #pragma unroll
         for (int x = 0; x < R; ++x) {
-            const int r = r0 + 8 * x + (lane & 7), gt = r & (kTreeM - 1), t = (rt * NG + r / kTreeM) * a.toks + gt / a.G;
-            if (r >= a.rows_cap || gt >= a.toks * a.G || t >= e.fresh) continue;
+            if (!live[x]) continue;
+            const int r = r0 + 8 * x + (lane & 7), gt = r & (kTreeM - 1), t = token(r);
             const float inv = s_inv[8 * x + (lane & 7)];
             uint16_t *to = a.out + ((size_t)i * a.T + t) * a.out_stride + (size_t)(g * a.G + gt % a.G) * D;
             *reinterpret_cast<uint2 *>(to + c4 * 4) =

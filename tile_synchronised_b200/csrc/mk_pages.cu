@@ -12,7 +12,11 @@
 // sequence (a table has at most 1024 rows): what they have to order (which
 // sequence gets which page, which of several sharers of a page copies it) is
 // a prefix sum over the list.  The data kernels (copies of whole pages, moves
-// of positions) run on all SMs and are bound by HBM.
+// of positions) run on all SMs and are bound by HBM.  Freeing, forking and
+// reserving 24 sequences with a copy of every last page (16 layers, 99 MB read
+// and written): 23.5 us; cutting, reserving, copying and compacting 16 drafts (32
+// layers, 249 MB): 46 us, 0.84 of the measured copy; with hardly any data: 10 us,
+// the four launches.
 #include <atomic>
 #include <cstdio>
 

