@@ -552,7 +552,8 @@ mk_status mk_pages_copy(const mk_pages *dst, const mk_pages *src, const int32_t 
                         int n, void *stream);
 /* The first error the pool's kernels recorded since the last call, which
  * clears it: MK_OK, MK_ERR_INVALID, MK_ERR_STATE (not enough free pages) or
- * MK_ERR_TIMEOUT, with the reason in mk_last_error(NULL).  Waits for `stream`. */
+ * MK_ERR_TIMEOUT, with the reason in mk_last_error(NULL).  Waits for `stream`;
+ * MK_ERR_STATE while it is being captured. */
 mk_status mk_pages_status(const mk_pages *pages, void *stream);
 
 /* The pass from the QKV projection to the attention: RMSNorm of every q and k

@@ -473,3 +473,21 @@ def test_offsets_behind_32_bits():
     b.copy(src, dst)
     b.check()
     assert torch.equal(kv[:, :, 0], kv[:, :, pages - n]) and torch.equal(kv[:, :, 1], kv[:, :, pages - 1])
+
+
+def test_a_check_during_a_capture_is_refused():
+    import tile_synchronised_b200 as mk
+    pool = filled([20, 5], [0, 0], layers=1, spare=4, seed=9)
+    cache = pool.to_cache()
+    seqs, counts = ints(0, 1), ints(12, 27)  # up to the table's 32 positions
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.reserve(seqs, counts)
+        with pytest.raises(mk.MkError, match="captured"):
+            cache.check()
+    pool.same_as(cache)
+    graph.replay()
+    cache.check()
+    pool.reserve([0, 1], [12, 27])
+    pool.same_as(cache)

@@ -585,7 +585,11 @@ extern "C" mk_status mk_pages_status(const mk_pages *p, void *stream) {
     if (st != MK_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int32_t w[4] = {0, 0, 0, 0};
-    cudaError_t e = cudaMemcpyAsync(w, p->state, sizeof w, cudaMemcpyDeviceToHost, s);
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(s, &capture);
+    if (e == cudaSuccess && capture != cudaStreamCaptureStatusNone)  // a wait would end the capture
+        return pages_refuse("pages_status", "the stream is being captured", MK_ERR_STATE);
+    if (e == cudaSuccess) e = cudaMemcpyAsync(w, p->state, sizeof w, cudaMemcpyDeviceToHost, s);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e == cudaSuccess && w[kStErr]) e = cudaMemsetAsync(p->state, 0, sizeof w, s);
     if (e != cudaSuccess) return pages_launched(e, "pages_status");
