@@ -600,6 +600,12 @@ mk_status mk_attention_tree(const mk_pages *pages, int layer, const void *q, lon
                             long long out_stride, void *scratch, size_t scratch_bytes, void *stream);
 size_t mk_attention_tree_scratch_bytes(int T, int n_heads, int n_kv_heads, int head_dim);
 
+/* Test hook: the time limit of a device-side wait in later mk_attention_tree
+ * calls of this process (0: the default of 2 s), and whether each CTA's first Q
+ * is left out (drop_q = 1), so that the wait for it runs out.  Used to test
+ * timeout reporting.  A captured call keeps what was set at its capture. */
+mk_status mk_debug_attention_tree_wait(unsigned long long wait_ns, int drop_q);
+
 #ifdef __cplusplus
 }
 #endif

@@ -292,3 +292,30 @@ def test_bad_entries_are_reported_and_leave_their_rows():
     mk.attention_tree(q.cuda(), cache, 0, torch.arange(2, dtype=torch.int32).cuda())
     with pytest.raises(mk.MkError, match="no page"):
         cache.check()
+
+
+@pytest.mark.parametrize("T,d", [(1, 64), (70, 128), (9, 256)])  # two groups on one tile, two row tiles, one group
+def test_a_wait_that_runs_out_is_reported(T, d):
+    """Every CTA's first Q is left out: its K and V are all on their way by the
+    time the wait for it runs out.  The rows are NaN, the status says so, and the
+    next call is as before."""
+    import tile_synchronised_b200 as mk
+    from tile_synchronised_b200 import _lib
+    lib = mk.load()
+    pool, q, new = make([300, 5], T, 8, 2, d, 16, torch.bfloat16, 61)
+    cache = pool.to_cache()
+    seqs = torch.arange(2, dtype=torch.int32).cuda()
+    good = mk.attention_tree(q.cuda(), cache, 0, seqs)
+    cache.check()
+    assert lib.mk_debug_attention_tree_wait(20_000_000, 1) == _lib.MK_OK  # 20 ms
+    try:
+        bad = mk.attention_tree(q.cuda(), cache, 0, seqs)
+        with pytest.raises(mk.MkError, match="ran out") as e:
+            cache.check()
+    finally:
+        assert lib.mk_debug_attention_tree_wait(0, 0) == _lib.MK_OK
+    assert e.value.status == _lib.MK_ERR_TIMEOUT
+    assert torch.isnan(bad).all()
+    again = mk.attention_tree(q.cuda(), cache, 0, seqs)
+    cache.check()
+    assert torch.equal(again, good)

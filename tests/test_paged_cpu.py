@@ -155,3 +155,9 @@ def test_pool_class_clone_is_independent():
     q = p.clone()
     q.kv.zero_()
     assert p.kv.abs().sum() > 0
+
+
+def test_the_wait_hook_checks_its_argument():
+    lib = _lib.load()
+    assert lib.mk_debug_attention_tree_wait(0, 2) == INVALID
+    assert lib.mk_debug_attention_tree_wait(0, 0) == OK

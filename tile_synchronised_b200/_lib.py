@@ -35,7 +35,7 @@ EXPORTS = ("mk_create", "mk_destroy", "mk_last_error", "mk_workspace_bytes", "mk
            "mk_tcdec_status", "mk_tcdec_last_error", "mk_tcdec_destroy", "mk_tcdec_set_graph",
            "mk_pages_state_bytes", "mk_pages_reserve", "mk_pages_fork", "mk_pages_compact", "mk_pages_free",
            "mk_pages_copy", "mk_pages_status", "mk_qk_norm_rope", "mk_attention_tree",
-           "mk_attention_tree_scratch_bytes")
+           "mk_attention_tree_scratch_bytes", "mk_debug_attention_tree_wait")
 
 
 class MkConfig(C.Structure):
@@ -145,6 +145,7 @@ def load() -> C.CDLL:
                              vp], st),
         "mk_attention_tree": ([pg, i32, vp, ll, i32, i32, i32, vp, vp, vp, vp, ll, vp, sz, vp], st),
         "mk_attention_tree_scratch_bytes": ([i32, i32, i32, i32], sz),
+        "mk_debug_attention_tree_wait": ([C.c_ulonglong, i32], st),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)

@@ -85,6 +85,8 @@ struct TreeArgs {
     int n, T, words, nq, G, seg, stages, q_tiles, rows_cap;
     int toks;        // new tokens of a row tile: 128 / G
     float scale;     // log2(e) / sqrt(d)
+    int drop_q;      // tests of the time limit: the first run's Q is never loaded
+    uint64_t wait_ns;  // time limit of a wait
 };
 
 // A listed sequence.
@@ -104,7 +106,7 @@ struct TreeRun {
 // Shared memory behind the operand tiles.
 struct TreeShared {
     uint64_t full[kTreeMaxStages], empty[kTreeMaxStages];
-    uint64_t s_full[2], p_full[2], pv_done[2], q_full, q_empty;
+    uint64_t s_full[2], p_full[2], pv_done[2], q_full, q_empty, mma_end;
     TreeRun first, run[10];  // where the walk begins; of each warp
     float2 ml[2][kTreeM];    // the groups' maxima (scaled) and sums at the end of a run
     uint32_t tmem;
@@ -484,6 +486,7 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
         }
         mbar_init(&sh.q_full, 1);
         mbar_init(&sh.q_empty, 1);
+        mbar_init(&sh.mma_end, 1);
         sh.abort = 0;
         sh.bad_v = 0;
         fence_barrier_init();
@@ -589,7 +592,7 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
             };
             // Q: 64 columns x G heads x tokens are the swizzled rows of an MMA operand
             auto load_q = [&]() {
-                if (seg_no && !tc_wait(&sh.q_empty, (seg_no - 1) & 1u, abort)) return false;
+                if (seg_no && !tc_wait(&sh.q_empty, (seg_no - 1) & 1u, abort, a.wait_ns)) return false;
                 if (lane == 0) {
                     const int tiles = two_rows() ? 2 : 1, tok = run.i * a.T + run.rt * NG * a.toks;
                     mbar_arrive_expect_tx(&sh.q_full, tiles * q_bytes);
@@ -603,7 +606,7 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
             };
             int tb = t0, pages = look(tb), next = look(tb + per);
             int off = (t0 * NT + my * seg) % ps;  // of this lane's part in its page
-            if (seg_no == 0) ok = load_q();
+            if (seg_no == 0 && !a.drop_q) ok = load_q();
             for (int t = t0; ok && t < t1; ++t) {
                 if (t - tb == per) {
                     tb = t;
@@ -621,7 +624,7 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
                 const uint32_t bytes = (uint32_t)(left < ns ? left : ns) * seg_bytes;
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv) {
-                    ok = __all_sync(0xFFFFFFFFu, tc_wait(&sh.empty[slot], phase, abort));
+                    ok = __all_sync(0xFFFFFFFFu, tc_wait(&sh.empty[slot], phase, abort, a.wait_ns));
                     if (!ok) break;
                     if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], bytes);
                     __syncwarp();
@@ -672,14 +675,14 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
                 if (j == jobs - 1) tc_commit(&sh.q_empty);
             };
             auto qk = [&](int j) {
-                if (!__all_sync(0xFFFFFFFFu, tc_wait(&sh.full[k_slot], k_phase, abort))) return false;
+                if (!__all_sync(0xFFFFFFFFu, tc_wait(&sh.full[k_slot], k_phase, abort, a.wait_ns))) return false;
                 tc_fence_after();
                 if (elect_one()) qk_issue(j);
                 __syncwarp();
                 if (!two || (j & 1)) step(k_slot, k_phase);
                 return true;
             };
-            ok = __all_sync(0xFFFFFFFFu, tc_wait(&sh.q_full, seg_no & 1u, abort));
+            ok = __all_sync(0xFFFFFFFFu, tc_wait(&sh.q_full, seg_no & 1u, abort, a.wait_ns));
             tc_fence_after();
             ok = ok && qk(0) && (jobs < 2 || qk(1));
 #pragma unroll 1
@@ -687,7 +690,8 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
                 const int b = j & 1;
                 // With K of job j + 2 there already, its S goes out right behind P V
                 const bool k_there = __all_sync(0xFFFFFFFFu, j + 2 < jobs && mbar_test_wait(&sh.full[k_slot], k_phase));
-                ok = tc_wait(&sh.full[v_slot], v_phase, abort) && tc_wait(&sh.p_full[b], used[b] & 1u, abort);
+                ok = tc_wait(&sh.full[v_slot], v_phase, abort, a.wait_ns) &&
+                     tc_wait(&sh.p_full[b], used[b] & 1u, abort, a.wait_ns);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 ++used[b];
@@ -741,7 +745,7 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
 #pragma unroll
                     for (int c = 0; c < NT / 32; ++c) bits[c] = live ? bits[c] : 0u;
                 }
-                ok = ok && tc_wait(&sh.s_full[b], seen[b] & 1u, abort);
+                ok = ok && tc_wait(&sh.s_full[b], seen[b] & 1u, abort, a.wait_ns);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 ++seen[b];
@@ -779,7 +783,7 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
                     }
                 }
                 if (NG == 1 && i > 0) {  // P V of the last tile (two groups: S came after it)
-                    ok = tc_wait(&sh.pv_done[0], done & 1u, abort);
+                    ok = tc_wait(&sh.pv_done[0], done & 1u, abort, a.wait_ns);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     ++done;
@@ -841,7 +845,7 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
                     // behind the last token, become zeros; with two row tiles
                     // by the first group, whose P V comes first
                     const int ld = load + 2 * i + 1, st = ld % S;
-                    ok = tc_wait(&sh.full[st], (ld / S) & 1u, abort);
+                    ok = tc_wait(&sh.full[st], (ld / S) & 1u, abort, a.wait_ns);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     const int pos = p0 + gt;
@@ -869,7 +873,7 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
             TreeOut w;
             w.mine = first < nt;  // this group had a tile (group 0 always has)
             if (ok && w.mine) {
-                ok = __all_sync(0xFFFFFFFFu, tc_wait(&sh.pv_done[grp], done & 1u, abort));
+                ok = __all_sync(0xFFFFFFFFu, tc_wait(&sh.pv_done[grp], done & 1u, abort, a.wait_ns));
                 ++done;
             }
             load += 2 * nt;
@@ -920,18 +924,29 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
             if (join) softmax_sync<NG>();  // O and the maxima have been read
         }
     }
-    // After a wait ran out some copies may be in flight: let the last one of
-    // every stage land before the shared memory is freed.
-    __syncwarp();
-    if (warp == kLoader && lane == 0 && *abort) {
-        for (int x = issued > S ? issued - S : 0; x < issued; ++x)
-            tc_drain(&sh.full[x % S], (uint32_t)(x / S) & 1u, kTcTimeoutNs);
-        if (q_issued) tc_drain(&sh.q_full, (uint32_t)(q_issued - 1) & 1u, kTcTimeoutNs);
-        pages_fail(a.p.state, kPgTimeout, 0, blockIdx.x);
-    }
+    // After a wait ran out some copies and MMAs may be in flight.  Which role's
+    // it was, and whether any, is known once all of them have ended: then the
+    // last copy of every stage and the last MMA are waited for, before the
+    // shared and the tensor memory are freed.
     tc_fence_before();
     __syncthreads();
+    if (*abort) {
+        if (warp == kLoader && lane == 0) {
+            for (int x = issued > S ? issued - S : 0; x < issued; ++x)
+                tc_drain(&sh.full[x % S], (uint32_t)(x / S) & 1u, kTcTimeoutNs);
+            if (q_issued) tc_drain(&sh.q_full, (uint32_t)(q_issued - 1) & 1u, kTcTimeoutNs);
+            pages_fail(a.p.state, kPgTimeout, 0, blockIdx.x);
+        }
+        __syncwarp();
+        if (warp == kIssuer) {
+            if (elect_one()) tc_commit(&sh.mma_end);
+            __syncwarp();
+            tc_drain(&sh.mma_end, 0u, kTcTimeoutNs);
+        }
+        __syncthreads();
+    }
     if (warp == kIssuer) {
+        __syncwarp();
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
     }
@@ -1083,6 +1098,10 @@ static int tree_grid() {
     return sms < kTreeMaxCtas ? sms : kTreeMaxCtas;
 }
 
+// What mk_debug_attention_tree_wait set.
+static std::atomic<unsigned long long> tree_wait_ns{kTcTimeoutNs};
+static std::atomic<int> tree_drop_q{0};
+
 static size_t tree_scratch(int T, int nq, int nkv, int d, int grid) {
     return (size_t)2 * grid * tree_rows_cap(T, nq / nkv, d) * (d + 2) * sizeof(float);
 }
@@ -1132,6 +1151,13 @@ extern "C" size_t mk_attention_tree_scratch_bytes(int T, int n_heads, int n_kv_h
     return tree_scratch(T, n_heads, n_kv_heads, head_dim, tree_grid());
 }
 
+extern "C" mk_status mk_debug_attention_tree_wait(unsigned long long wait_ns, int drop_q) {
+    if (drop_q != 0 && drop_q != 1) return pages_refuse("debug_attention_tree_wait", "drop_q must be 0 or 1");
+    tree_wait_ns.store(wait_ns ? wait_ns : kTcTimeoutNs, std::memory_order_relaxed);
+    tree_drop_q.store(drop_q, std::memory_order_relaxed);
+    return MK_OK;
+}
+
 extern "C" mk_status mk_attention_tree(const mk_pages *p, int layer, const void *q, long long q_stride, int n, int T,
                                        int n_heads, const int32_t *seqs, const int32_t *n_new, const uint32_t *mask,
                                        void *out, long long out_stride, void *scratch, size_t scratch_bytes,
@@ -1175,6 +1201,8 @@ extern "C" mk_status mk_attention_tree(const mk_pages *p, int layer, const void 
     a.part_o = static_cast<float4 *>(scratch);
     a.part_ml = reinterpret_cast<float2 *>(a.part_o + (size_t)2 * grid * a.rows_cap * (d / 4));
     a.scale = (float)(1.4426950408889634 / std::sqrt((double)d));
+    a.wait_ns = tree_wait_ns.load(std::memory_order_relaxed);
+    a.drop_q = tree_drop_q.load(std::memory_order_relaxed);
     // a copy covers the part of a tile that lies in one page
     const int nt = tree_nt(d);
     int seg = nt;

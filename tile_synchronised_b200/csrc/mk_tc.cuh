@@ -53,14 +53,15 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, i
 
 // Bounded wait for the phase `parity` of an mbarrier; false after the time
 // limit or once another role of the CTA has given up.
-__device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+__device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                        uint64_t limit_ns = kTcTimeoutNs) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t it = 1;; ++it) {
         if (mbar_try_wait_sleep(bar, parity, 10000u)) return true;
         if ((it & 7u) == 0u) {
             if (*abort) return false;
-            if (globaltimer_ns() - t0 > kTcTimeoutNs) {
+            if (globaltimer_ns() - t0 > limit_ns) {
                 *abort = 1;
                 return false;
             }
