@@ -288,3 +288,19 @@ def test_attention_chunk_rule_needs_no_device():
     assert ch(4, 8, 32768) == 9       # 288 CTAs, one wave of 2 per SM
     assert ch(1, 8, 32768) == 34      # the first count whose wave is 90 % full: 272 of 296 slots
     assert ch(0, 8, 1024) == 0 and ch(1, 0, 1024) == 0 and ch(1, 8, 0) == 0
+
+
+VECTORS = r"(?:float2|float4|uint2|uint4|int2|int4|ulonglong2|longlong2)"
+
+
+def test_shared_arrays_read_as_vectors_are_declared_aligned():
+    """A static shared array that a kernel reads through a vector type has an
+    alignment of its own: the element type's does not cover it."""
+    found = 0
+    for path in mkbuild.sources():
+        text = open(path).read()
+        for name in set(re.findall(r"reinterpret_cast<(?:const )?(?:volatile )?" + VECTORS + r" \*>\(&?(\w+)[\[\)]", text)):
+            for line in re.findall(r"^.*__shared__[^;]*\b%s\b[^;]*;" % name, text, flags=re.M):
+                found += 1
+                assert "align" in line or re.search(r"__shared__ " + VECTORS, line), f"{os.path.basename(path)}: {line.strip()}"
+    assert found >= 2

@@ -70,7 +70,7 @@ __device__ __forceinline__ float4 scale4(const float4 &x, float s) {
 template <int D, bool F32, bool BF16, int TOK>
 __global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(const __grid_constant__ RopeArgs a) {
     constexpr int LR = D / 8, kSubs = kRopeThreads / LR;  // lanes of a head, heads at a time
-    __shared__ float s_cos[TOK][D / 2], s_sin[TOK][D / 2];
+    __shared__ __align__(16) float s_cos[TOK][D / 2], s_sin[TOK][D / 2];  // read 4 at a time
     __shared__ size_t s_row[TOK];  // offset of the token's slot in its layer's K or V
     __shared__ int s_write[TOK];
     const int chunks = (a.T + TOK - 1) / TOK, i = blockIdx.x / chunks, t0 = (blockIdx.x - i * chunks) * TOK;
