@@ -319,3 +319,13 @@ def test_a_wait_that_runs_out_is_reported(T, d):
     again = mk.attention_tree(q.cuda(), cache, 0, seqs)
     cache.check()
     assert torch.equal(again, good)
+
+
+def test_tree_mask_on_the_gpu_reads_no_index_outside_a_row():
+    """Parents that are no smaller index count as -1 there."""
+    import tile_synchronised_b200 as mk
+    parents = [random_tree(40, 3), random_tree(40, 4)]
+    odd = torch.tensor(parents)
+    odd[0, 7], odd[0, 8], odd[1, 0], odd[1, 39] = 40, 8, 5, -3
+    parents[0][7] = parents[0][8] = parents[1][0] = parents[1][39] = -1
+    assert torch.equal(mk.tree_mask(odd.cuda()).cpu(), pack_bits(torch.stack([visible(p) for p in parents])))

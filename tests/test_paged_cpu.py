@@ -161,3 +161,12 @@ def test_the_wait_hook_checks_its_argument():
     lib = _lib.load()
     assert lib.mk_debug_attention_tree_wait(0, 2) == INVALID
     assert lib.mk_debug_attention_tree_wait(0, 0) == OK
+
+
+@pytest.mark.parametrize("parents", [[[-1, 1]], [[-1, 2]], [[0, 0]], [[-1, 0, 1], [-1, 0, -2]], [[-1, 0, 10 ** 6]]])
+def test_tree_mask_refuses_parents_that_do_not_come_first(parents):
+    with pytest.raises(ValueError, match="smaller index"):
+        mk.tree_mask(torch.tensor(parents))
+    for wrong in (torch.tensor([-1, 0]), torch.tensor([[-1.0, 0.0]])):
+        with pytest.raises(ValueError, match="integers"):
+            mk.tree_mask(wrong)

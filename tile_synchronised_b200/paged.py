@@ -173,9 +173,17 @@ class PagedCache:
 def tree_mask(parents: torch.Tensor) -> torch.Tensor:
     """The mask of attention_tree (int32 bits [n, T, (T + 31) // 32]) of trees
     given by parents [n, T]: the index of each token's parent, smaller than its
-    own, or -1 for a child of the last committed token."""
+    own, or -1 for a child of the last committed token.  Other parents are
+    refused on the CPU; on a GPU, where looking would wait for it, they count
+    as -1."""
+    if parents.dim() != 2 or parents.is_floating_point():
+        raise ValueError("parents must be integers [n, T]")
     n, T = parents.shape
     p = parents.long()
+    good = (p >= -1) & (p < torch.arange(T, device=p.device))
+    if not p.is_cuda and not good.all():
+        raise ValueError("a parent must be -1 or a smaller index than its child's")
+    p = torch.where(good, p, -1)  # no index leaves its row
     seen = torch.eye(T, dtype=torch.bool, device=p.device).repeat(n, 1, 1)
     rows = torch.arange(n, device=p.device)
     for t in range(1, T):  # a row's parent comes before it and is complete
