@@ -504,8 +504,9 @@ size_t mk_attention_noalloc_limit_bytes(void);
  * Lists (`seqs`, `counts`, ...) are device int32 arrays, read when the call's
  * kernels run, so captured calls follow their contents.  What only the device
  * can see (an index out of range, a sequence listed twice, no free page, ...)
- * leaves that entry undone and is recorded in `state`, the first one until
- * mk_pages_status reads it; the other entries are done.  Calls that change a
+ * leaves that entry undone, unless its call says otherwise, and is recorded in
+ * `state`, the first one until mk_pages_status reads it; the other entries are
+ * done.  Calls that change a
  * pool must be ordered with each other and with the calls that read it.  All
  * are asynchronous on `stream` and allocate nothing.  Errors on the host:
  * MK_ERR_INVALID, MK_ERR_UNSUPPORTED (head_dim, dtype, page_size),
@@ -571,7 +572,7 @@ mk_status mk_pages_status(const mk_pages *pages, void *stream);
  * [head_dim] or NULL.  q: token (i, t) at q + (i T + t) * q_stride.  Strides
  * are multiples of 8, pointers 16-byte aligned.  A sequence may occur once.
  * A slot without a page, or in a page held by another sequence too, is not
- * written (mk_pages_status tells). */
+ * written (mk_pages_status tells); q and the entry's other slots are. */
 mk_status mk_qk_norm_rope(const mk_pages *pages, int layer, const void *qkv, int qkv_dtype, long long qkv_stride,
                           int n, int T, int n_heads, const int32_t *seqs, const int32_t *n_new, const int32_t *depth,
                           const void *q_gain, const void *k_gain, float eps, double theta, void *q,
@@ -585,8 +586,10 @@ mk_status mk_qk_norm_rope(const mk_pages *pages, int layer, const void *qkv, int
  * mask: device uint32 [n][T][(T + 31) / 32], bit u % 32 of word u / 32 (a
  * tree: a token's ancestors and itself); NULL: u <= t (a chunk of a prompt;
  * T = 1: a decode step).  A row that sees nothing is 0.  An infinity or NaN in
- * K or V at a position that a row does not see does not reach it.  Rows
- * t >= n_new[i] of out are left as they were.  q, out: the cache's type, token
+ * K or V at a position that a row does not see does not reach it.  Where a
+ * position has no page, the rows that see it are NaN, and rows that are worked
+ * on with them may be (mk_pages_status tells).  Rows t >= n_new[i] of out are
+ * left as they were.  q, out: the cache's type, token
  * (i, t) at (i T + t) * stride elements (multiples of 8), n_heads x head_dim
  * values each, 16-byte aligned; out must not overlap q.  A sequence may occur
  * several times; n <= 1024.

@@ -329,3 +329,53 @@ def test_tree_mask_on_the_gpu_reads_no_index_outside_a_row():
     odd[0, 7], odd[0, 8], odd[1, 0], odd[1, 39] = 40, 8, 5, -3
     parents[0][7] = parents[0][8] = parents[1][0] = parents[1][39] = -1
     assert torch.equal(mk.tree_mask(odd.cuda()).cpu(), pack_bits(torch.stack([visible(p) for p in parents])))
+
+
+@pytest.mark.parametrize("page", [-1, 10 ** 6])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_rows_that_see_a_missing_page_are_nan(d, page):
+    """Many sequences, several to a CTA, some with a hole: all their rows are
+    NaN, no other row is touched by it, and the next call is as before."""
+    import tile_synchronised_b200 as mk
+    n, T = 60, 3
+    lengths = [20 + (41 * i) % 300 for i in range(n)]
+    pool, q, new = make(lengths, T, 8, 4, d, 16, torch.bfloat16, 62)
+    cache = pool.to_cache()
+    seqs = torch.arange(n, dtype=torch.int32).cuda()
+    good = mk.attention_tree(q.cuda(), cache, 0, seqs)
+    cache.check()
+    was = cache.table.clone()
+    holes = [0, 7, 8, 31, 59]
+    for k, s in enumerate(holes):
+        cache.table[s, (k * 3) % ((lengths[s] + 15) // 16)] = page
+    got = mk.attention_tree(q.cuda(), cache, 0, seqs)
+    with pytest.raises(mk.MkError, match="no page"):
+        cache.check()
+    rest = [i for i in range(n) if i not in holes]
+    assert torch.isnan(got[holes]).all()
+    assert torch.equal(got[rest], good[rest])
+    cache.table.copy_(was)
+    assert torch.equal(mk.attention_tree(q.cuda(), cache, 0, seqs), good)
+    cache.check()
+
+
+def test_a_long_sequence_with_a_missing_page():
+    """One sequence over many CTAs, hole in the middle: every row NaN.  A hole
+    among the new tokens of a chunk: the row tiles before it are right."""
+    import tile_synchronised_b200 as mk
+    pool, q, new = make([9000], 4, 4, 2, 128, 16, torch.bfloat16, 63)
+    cache = pool.to_cache()
+    cache.table[0, 250] = -1
+    got = mk.attention_tree(q.cuda(), cache, 0, torch.zeros(1, dtype=torch.int32).cuda())
+    with pytest.raises(mk.MkError, match="no page"):
+        cache.check()
+    assert torch.isnan(got).all()
+    pool, q, new = make([100], 500, 4, 2, 64, 16, torch.bfloat16, 64)  # row tiles of 64 new tokens, two at a time
+    cache = pool.to_cache()
+    good = mk.attention_tree(q.cuda(), cache, 0, torch.zeros(1, dtype=torch.int32).cuda())
+    cache.check()
+    cache.table[0, 25] = -1  # new tokens 300 .. 315
+    got = mk.attention_tree(q.cuda(), cache, 0, torch.zeros(1, dtype=torch.int32).cuda())
+    with pytest.raises(mk.MkError, match="no page"):
+        cache.check()
+    assert torch.isnan(got[0, 300:]).all() and torch.equal(got[0, :256], good[0, :256])

@@ -110,7 +110,8 @@ struct TreeShared {
     TreeRun first, run[10];  // where the walk begins; of each warp
     float2 ml[2][kTreeM];    // the groups' maxima (scaled) and sums at the end of a run
     uint32_t tmem;
-    int abort, bad_v, pad;
+    int abort, bad_v;
+    int bad_page[4];         // [r % 4] = r + 1: a page of the CTA's run r is missing
 };
 
 // Row tiles of entry e, and the tiles of positions that row tile rt needs:
@@ -489,6 +490,7 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
         mbar_init(&sh.mma_end, 1);
         sh.abort = 0;
         sh.bad_v = 0;
+        for (int s = 0; s < 4; ++s) sh.bad_page[s] = 0;
         fence_barrier_init();
     }
     if (warp == kIssuer) {
@@ -618,8 +620,12 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
                 const bool go = mine && pos < end;
                 if (go && (page < 0 || page >= a.p.n_pages)) {
                     pages_fail(a.p.state, kPgPosition, run.i, pos);
+                    // the run's rows become NaN.  By the softmax's epilogue of a run the loader is three runs
+                    // ahead at most: the third one's Q waits for S of the second, and that for P of the first
+                    *reinterpret_cast<volatile int *>(&sh.bad_page[seg_no & 3]) = seg_no + 1;
                     page = -1;  // out of the tensor: zeros
                 }
+                __syncwarp();
                 const int head = page < 0 ? -1 : page * nkv + g, left = (end - t * NT + seg - 1) >> seg_log;
                 const uint32_t bytes = (uint32_t)(left < ns ? left : ns) * seg_bytes;
 #pragma unroll 1
@@ -722,7 +728,7 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
         const int grp = warp >> 2, gw = warp & 3;  // gw: its tensor-memory lanes
         const int gt = gw * 32 + lane;             // row within the group's 128
         const uint32_t lanes = tmem + ((uint32_t)(gw * 32) << 16);
-        int load = 0;  // ring loads of earlier runs
+        int load = 0, no = 0;  // ring loads of earlier runs, and their number
         uint32_t seen[2] = {0, 0}, done = 0;  // S of each buffer taken, P V waited for
         bool ok = true;
         const int my_tok = gt / a.G, my_g = gt - my_tok * a.G;
@@ -877,14 +883,16 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
                 ++done;
             }
             load += 2 * nt;
+            const bool fine = ok && *reinterpret_cast<volatile int *>(&sh.bad_page[no & 3]) != no + 1;
+            ++no;
             const float nan = CUDART_NAN_F;
             if (join) {
-                sh.ml[grp][gt] = ok ? make_float2(m * a.scale, l) : make_float2(nan, nan);
+                sh.ml[grp][gt] = fine ? make_float2(m * a.scale, l) : make_float2(nan, nan);
                 tc_fence_before();
                 softmax_sync<NG>();
             }
             tc_fence_after();
-            w.ok = ok;
+            w.ok = fine;
             w.join = join;
             w.live = live;
             w.whole = run.t0 == 0 && run.t1 == run.tiles;
@@ -918,7 +926,8 @@ __global__ void __launch_bounds__(tree_threads(D), 1)
                 else
                     tree_write<D, BF16, false>(a, run, w);
                 if (live && !w.whole && (!join || grp == 0))
-                    a.part_ml[(size_t)run.slot * a.rows_cap + (two ? grp * kTreeM : 0) + gt] = ok ? make_float2(w.m2, l) : make_float2(nan, nan);
+                    a.part_ml[(size_t)run.slot * a.rows_cap + (two ? grp * kTreeM : 0) + gt] =
+                        fine ? make_float2(w.m2, l) : make_float2(nan, nan);
             }
             tc_fence_before();
             if (join) softmax_sync<NG>();  // O and the maxima have been read

@@ -259,7 +259,8 @@ def attention_tree(q: torch.Tensor, cache: PagedCache, layer: int, seqs: torch.T
     committed positions and the new tokens whose bit is set in its row of mask
     (int32 bits [n, T, (T + 31) // 32], see tree_mask), by default those up to
     itself (T = 1: a decode step).  Returns `out` (like q); its rows t >=
-    n_new[i] are not written."""
+    n_new[i] are not written, and those that see a position without a page are
+    NaN."""
     if q.dim() != 4:
         raise ValueError("q must be [n, T, n_heads, head_dim]")
     n, T, nq, d = q.shape
