@@ -491,3 +491,16 @@ def test_a_check_during_a_capture_is_refused():
     cache.check()
     pool.reserve([0, 1], [12, 27])
     pool.same_as(cache)
+
+
+def test_a_reserve_behind_a_page_outside_the_pool_is_left_undone():
+    import tile_synchronised_b200 as mk
+    pool = filled([20, 33], [28, 3], layers=1, spare=8, extra=1, poison=False, seed=10)
+    pool.refs[pool.table[0, 2]] = 0  # the row ends behind the partly filled page
+    pool.table[0, 1:] = torch.tensor([99, -1], dtype=torch.int32)
+    cache = pool.to_cache()
+    cache.reserve(ints(0, 1, 2), ints(28, 15, 17))
+    with pytest.raises(mk.MkError, match="page index"):
+        cache.check()
+    pool.reserve([1, 2], [15, 17])
+    pool.same_as(cache)

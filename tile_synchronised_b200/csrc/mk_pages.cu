@@ -104,10 +104,12 @@ __global__ void __launch_bounds__(kMgThreads, 1)
             need = last - lo;
             if (e.len % ps && lo > first) {
                 const int page = row[first];
-                if (page < p.n_pages)
+                if (page < p.n_pages) {
                     shared = page;
-                else
+                } else {  // the committed positions on it are lost: no new ones behind them
                     pages_fail(p.state, kPgPage, i, page);
+                    need = 0;
+                }
             }
             s_first[i] = first;
             s_miss[i] = lo;
