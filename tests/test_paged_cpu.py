@@ -1,6 +1,9 @@
 """Host-side checks of the paged-cache entry points: refusals before any
 launch, the tree mask, and the plain implementations the GPU tests use."""
 import ctypes as C
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -170,3 +173,16 @@ def test_tree_mask_refuses_parents_that_do_not_come_first(parents):
     for wrong in (torch.tensor([-1, 0]), torch.tensor([[-1.0, 0.0]])):
         with pytest.raises(ValueError, match="integers"):
             mk.tree_mask(wrong)
+
+
+def test_the_package_imports_without_cuda_in_torch():
+    """A torch built without CUDA lacks the private names that shorten a call."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = ("import torch\n"
+            "for name in ('_cuda_getCurrentRawStream', '_cuda_getDevice'):\n"
+            "    if hasattr(torch._C, name): delattr(torch._C, name)\n"
+            "import tile_synchronised_b200 as mk\n"
+            "print(mk.tree_mask(torch.tensor([[-1, 0, 0]])).tolist())\n")
+    out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert out.returncode == 0, out.stderr
+    assert out.stdout.strip() == "[[[1], [3], [5]]]"

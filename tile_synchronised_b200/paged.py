@@ -24,8 +24,13 @@ from ._lib import MK_BF16, MK_FP16, MK_FP32, MkPages, check, load
 _TYPES = {torch.bfloat16: MK_BF16, torch.float16: MK_FP16, torch.float32: MK_FP32}
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream().cuda_stream without its 2 us
-_get_device = torch._C._cuda_getDevice  # current_device() without its check of the initialisation
+def _public_raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# The same without 2 us of checks and objects a call, where this torch has them (one built without CUDA does not).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_raw_stream)
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _INT32 = torch.int32
 
 
