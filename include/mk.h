@@ -545,8 +545,8 @@ mk_status mk_pages_compact(const mk_pages *pages, const int32_t *seqs, const int
  * the pages behind them, reserved ones included. */
 mk_status mk_pages_free(const mk_pages *pages, const int32_t *seqs, const int32_t *lengths, int n, void *stream);
 /* Page dst_pages[k] of `dst` = page src_pages[k] of `src`, in every layer: the
- * same pool, or two with pages of the same shape and type (to move sequences
- * between pools).  Tables and counts are not touched.  A pair is left out when
+ * same pool (kv and n_pages), or two with pages of the same shape and type and
+ * no byte in common (to move sequences between pools).  Tables and counts are not touched.  A pair is left out when
  * its destination occurs twice or, within one pool, its source is written by
  * the same call. */
 mk_status mk_pages_copy(const mk_pages *dst, const mk_pages *src, const int32_t *src_pages, const int32_t *dst_pages,

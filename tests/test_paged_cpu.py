@@ -186,3 +186,16 @@ def test_the_package_imports_without_cuda_in_torch():
     out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
     assert out.returncode == 0, out.stderr
     assert out.stdout.strip() == "[[[1], [3], [5]]]"
+
+
+def test_copies_between_overlapping_pools_are_refused():
+    """2 layers x 8 pages x 2 heads x 16 x 64 values: 128 KiB of K and V."""
+    lib = _lib.load()
+    size = 2 * 2 * 8 * 2 * 16 * 64 * 2
+    at = 1 << 20
+    a = pages(kv=at)
+    for kv, n in ((at + 16, 8), (at + size - 16, 8), (at - 16, 8), (at - size // 2 + 16, 4), (at, 7), (at, 9)):
+        for dst, src in ((a, pages(kv=kv, n_pages=n)), (pages(kv=kv, n_pages=n), a)):
+            assert lib.mk_pages_copy(dst, src, None, None, 0, None) == INVALID and "overlap" in reason()
+    for kv, n in ((at, 8), (at + size, 8), (at - size // 2, 4)):  # the same pool, and neighbours
+        assert lib.mk_pages_copy(a, pages(kv=kv, n_pages=n), None, None, 0, None) == OK

@@ -490,6 +490,10 @@ static const char *pages_message(int code) {
     }
 }
 
+static size_t pages_bytes(const mk_pages &p) {
+    return (size_t)2 * p.n_layers * p.n_pages * p.n_kv_heads * p.page_size * p.head_dim * 2;
+}
+
 // A list of n sequences: 0 means nothing to do.
 static mk_status pages_list(const mk_pages *p, int n, const void *a, const void *b, const char *who) {
     const mk_status st = pages_check(p, -1, who);
@@ -567,6 +571,11 @@ extern "C" mk_status mk_pages_copy(const mk_pages *dst, const mk_pages *src, con
         return pages_refuse("pages_copy", "the pools' pages must have the same shape and type");
     if (n < 0 || n > dst->n_pages || (n && (!src_pages || !dst_pages)))
         return pages_refuse("pages_copy", "needs 0 <= n <= n_pages and two lists");
+    // The kernel takes two pools for one where their pages are the same bytes; other pools must have no byte in common.
+    const bool same = dst->kv == src->kv && dst->n_pages == src->n_pages;
+    const uintptr_t d0 = (uintptr_t)dst->kv, s0 = (uintptr_t)src->kv;
+    if (!same && d0 < s0 + pages_bytes(*src) && s0 < d0 + pages_bytes(*dst))
+        return pages_refuse("pages_copy", "the pools overlap and are not the same pool");
     if (n == 0) return MK_OK;
     const int smem = 2 * ((dst->n_pages + 31) / 32) * 4;
     if (smem > 48 * 1024) {

@@ -161,7 +161,8 @@ class PagedCache:
 
     def copy(self, src_pages: torch.Tensor, dst_pages: torch.Tensor, source: "PagedCache | None" = None,
              stream=None) -> None:
-        """Page dst_pages[k] = page src_pages[k] of `source` (this cache by default), in every layer."""
+        """Page dst_pages[k] = page src_pages[k] of `source` (this cache by
+        default; one whose kv has no byte in common with this one's), in every layer."""
         n = src_pages.numel()
         src = self if source is None else source
         if src.device != self.device:
