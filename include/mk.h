@@ -569,8 +569,10 @@ mk_status mk_pages_status(const mk_pages *pages, void *stream);
  * then the v heads (the row of mk_linear_tc on stacked weights).  n_new: NULL
  * = T for all; tokens t >= n_new[i] are padding, nothing of theirs is written.
  * depth: [n][T] (a token's depth in its tree), NULL = t.  gains: bf16
- * [head_dim] or NULL.  q: token (i, t) at q + (i T + t) * q_stride.  Strides
- * are multiples of 8, pointers 16-byte aligned.  A sequence may occur once.
+ * [head_dim] or NULL.  q: token (i, t) at q + (i T + t) * q_stride; it must not
+ * overlap qkv, other than as the q heads of qkv themselves (same address, stride
+ * and type).  Strides are multiples of 8, pointers 16-byte aligned.  A sequence
+ * may occur once.
  * A slot without a page, or in a page held by another sequence too, is not
  * written (mk_pages_status tells); q and the entry's other slots are. */
 mk_status mk_qk_norm_rope(const mk_pages *pages, int layer, const void *qkv, int qkv_dtype, long long qkv_stride,
@@ -591,7 +593,8 @@ mk_status mk_qk_norm_rope(const mk_pages *pages, int layer, const void *qkv, int
  * on with them may be (mk_pages_status tells).  Rows t >= n_new[i] of out are
  * left as they were.  q, out: the cache's type, token
  * (i, t) at (i T + t) * stride elements (multiples of 8), n_heads x head_dim
- * values each, 16-byte aligned; out must not overlap q.  A sequence may occur
+ * values each, 16-byte aligned; out must not overlap q (rows of both may lie
+ * between each other's where the strides are equal).  A sequence may occur
  * several times; n <= 1024.
  * scratch: device, mk_attention_tree_scratch_bytes (for the current device's
  * SM count), 16-byte aligned, needs no initialisation; calls that share it

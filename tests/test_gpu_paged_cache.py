@@ -504,3 +504,32 @@ def test_a_reserve_behind_a_page_outside_the_pool_is_left_undone():
         cache.check()
     pool.reserve([1, 2], [15, 17])
     pool.same_as(cache)
+
+
+@pytest.mark.parametrize("n,T", [(2, 5), (8, 151)])
+def test_q_in_place_and_between_the_rows_of_qkv(n, T):
+    """q over qkv's own q heads, and q rows between the rows of qkv: the bits of
+    a q of its own.  The attention's result between the rows of its q."""
+    import tile_synchronised_b200 as mk
+    nq, nkv, d = 20, 4, 64
+    pool = filled([40 + i for i in range(n)], [T] * n, nkv=nkv, d=d, seed=37, poison=False)
+    a, b, c = (pool.to_cache() for _ in range(3))
+    width = (nq + 2 * nkv) * d
+    hold = torch.randn((n, T, width + nq * d), generator=generator(38)).to(torch.bfloat16).cuda()
+    qkv = hold[..., :width]
+    gain = (1 + 0.2 * torch.randn(d, generator=generator(39))).to(torch.bfloat16).cuda()
+    seqs = ints(list(range(n)))
+    ref = mk.qk_norm_rope(qkv.clone(), a, 0, seqs, nq, 10000.0, gain, gain)
+    between = hold[..., width:].view(n, T, nq, d)
+    assert torch.equal(mk.qk_norm_rope(qkv, b, 0, seqs, nq, 10000.0, gain, gain, out=between), ref)
+    over = hold[..., :nq * d].view(n, T, nq, d)
+    mk.qk_norm_rope(qkv, c, 0, seqs, nq, 10000.0, gain, gain, out=over)
+    assert torch.equal(over, ref)
+    for x in (a, b, c):
+        x.check()
+        assert torch.equal(x.kv, a.kv)
+    o = mk.attention_tree(ref, a, 0, seqs)
+    mk.attention_tree(between, a, 0, seqs, out=over)
+    assert torch.equal(over, o)
+    with pytest.raises(mk.MkError, match="overlap"):
+        mk.attention_tree(between, a, 0, seqs, out=hold[..., width - 8:-8].view(n, T, nq, d))

@@ -199,3 +199,31 @@ def test_copies_between_overlapping_pools_are_refused():
             assert lib.mk_pages_copy(dst, src, None, None, 0, None) == INVALID and "overlap" in reason()
     for kv, n in ((at, 8), (at + size, 8), (at - size // 2, 4)):  # the same pool, and neighbours
         assert lib.mk_pages_copy(a, pages(kv=kv, n_pages=n), None, None, 0, None) == OK
+
+
+def test_outputs_that_overlap_inputs_are_refused():
+    """No such call gets as far as a launch."""
+    lib, p = _lib.load(), pages()
+    at = 1 << 24
+
+    def rope(qkv, dt, qs, q, os, n=2, T=3):
+        return lib.mk_qk_norm_rope(p, 0, C.c_void_p(qkv), dt, qs, n, T, 4, PTR, None, None, None, None, 1e-6, 1e4,
+                                   C.c_void_p(q), os, None)
+
+    # rows of 8 heads of 64: 2048 bytes in fp32, 1024 in 16 bits; q rows of 4: 512
+    for args in ((at, 2, 512, at, 256), (at, 2, 512, at + 2032, 256), (at, 2, 512, at + 6 * 2048 - 16, 256),
+                 (at, 2, 512, at - 6 * 512 + 16, 256), (at, 2, 512, at, 1024), (at, 0, 512, at, 256),
+                 (at, 0, 512, at + 16, 512), (at, 0, 512, at + 512, 512), (at, 0, 1024, at + 1536 + 16, 1024),
+                 (at, 0, 1024, at - 496, 1024)):
+        assert rope(*args) == INVALID and "overlap" in reason(), args
+
+    def attend(q, qs, out, os, scratch=1 << 28, n=2, T=3):
+        return lib.mk_attention_tree(p, 0, C.c_void_p(q), qs, n, T, 4, PTR, None, None, C.c_void_p(out), os,
+                                     C.c_void_p(scratch), 1 << 26, None)
+
+    for args in ((at, 256, at, 256), (at, 256, at + 16, 256), (at, 256, at + 6 * 512 - 16, 256),
+                 (at, 256, at - 6 * 512 + 16, 256), (at, 512, at + 496, 512), (at, 512, at + 528, 512),
+                 (at, 512, at + 512, 256), (at + 2048 - 496, 512, at, 512)):
+        assert attend(*args) == INVALID and "out must not overlap q" in reason(), args
+    for scratch in (at, at + 5 * 512, at - 16, (1 << 25), (1 << 25) + 5 * 512):
+        assert attend(at, 256, 1 << 25, 256, scratch) == INVALID and "scratch must not" in reason(), scratch

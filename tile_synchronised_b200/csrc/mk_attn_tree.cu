@@ -56,6 +56,7 @@
 
 #include <atomic>
 #include <cmath>
+#include <utility>
 
 #include "mk_kernel.h"
 #include "mk_pages.h"
@@ -1189,6 +1190,13 @@ extern "C" mk_status mk_attention_tree(const mk_pages *p, int layer, const void 
     const int grid = tree_grid();
     if (scratch_bytes < tree_scratch(T, n_heads, p->n_kv_heads, d, grid))
         return pages_refuse(who, "scratch is smaller than mk_attention_tree_scratch_bytes");
+    const size_t rows = (size_t)n * T, width = (size_t)n_heads * d * 2;
+    if (pages_rows_meet(q, width, (size_t)q_stride * 2, out, width, (size_t)out_stride * 2, rows))
+        return pages_refuse(who, "out must not overlap q");
+    const size_t used = tree_scratch(T, n_heads, p->n_kv_heads, d, grid);
+    for (const auto &x : {std::make_pair(q, q_stride), std::make_pair((const void *)out, out_stride)})
+        if (pages_rows_meet(x.first, (rows - 1) * x.second * 2 + width, used, scratch, used, used, 1))
+            return pages_refuse(who, "scratch must not overlap q or out");
     TreeArgs a{};
     a.p = *p;
     a.q = static_cast<const uint16_t *>(q);
@@ -1219,12 +1227,12 @@ extern "C" mk_status mk_attention_tree(const mk_pages *p, int layer, const void 
         while (p->page_size % seg) seg /= 2;
     a.seg = seg;
     CUtensorMap mq, mk, mv;
-    const uint64_t rows = (uint64_t)p->n_pages * p->n_kv_heads;
+    const uint64_t heads = (uint64_t)p->n_pages * p->n_kv_heads;
     const uint32_t blocks = seg == nt ? (uint32_t)(d / 64) : 1u;
     if (!tc_make_map_heads(&mq, q, (uint64_t)n * T, (uint64_t)q_stride, (uint32_t)n_heads, (uint32_t)d, (uint32_t)a.G,
                            (uint32_t)a.toks) ||
-        !tc_make_map_pages(&mk, a.k, rows, (uint32_t)p->page_size, (uint32_t)d, (uint32_t)seg, blocks) ||
-        !tc_make_map_pages(&mv, a.v, rows, (uint32_t)p->page_size, (uint32_t)d, (uint32_t)seg, blocks)) {
+        !tc_make_map_pages(&mk, a.k, heads, (uint32_t)p->page_size, (uint32_t)d, (uint32_t)seg, blocks) ||
+        !tc_make_map_pages(&mv, a.v, heads, (uint32_t)p->page_size, (uint32_t)d, (uint32_t)seg, blocks)) {
         pages_refuse(who, "the driver refused the tensor map");
         return MK_ERR_CUDA;
     }

@@ -476,6 +476,15 @@ mk_status pages_launched(cudaError_t e, const char *who) {
     return MK_ERR_CUDA;
 }
 
+bool pages_rows_meet(const void *a, size_t width_a, size_t stride_a, const void *b, size_t width_b, size_t stride_b,
+                     size_t rows) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    if (x + (rows - 1) * stride_a + width_a <= y || y + (rows - 1) * stride_b + width_b <= x) return false;
+    if (stride_a != stride_b) return true;
+    const size_t ahead = x <= y ? (y - x) % stride_a : (stride_a - (x - y) % stride_a) % stride_a;
+    return ahead < width_a || ahead + width_b > stride_a;
+}
+
 static const char *pages_message(int code) {
     switch (code) {
         case kPgSeq: return "a sequence index is out of range or listed twice (entry, sequence)";

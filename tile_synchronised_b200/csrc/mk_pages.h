@@ -92,6 +92,11 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 mk_status pages_check(const mk_pages *p, int layer, const char *who);
 mk_status pages_refuse(const char *who, const char *why, mk_status st = MK_ERR_INVALID);
 mk_status pages_launched(cudaError_t e, const char *who);
+// `rows` rows of width_a bytes, stride_a bytes apart from a on, and as many from
+// b on: can they have a byte in common?  Exact where the strides are the same;
+// else rows that lie between each other's count as common.
+bool pages_rows_meet(const void *a, size_t width_a, size_t stride_a, const void *b, size_t width_b, size_t stride_b,
+                     size_t rows);
 int pages_sms();
 
 }  // namespace mk

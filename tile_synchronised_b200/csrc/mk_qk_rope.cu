@@ -207,6 +207,12 @@ extern "C" mk_status mk_qk_norm_rope(const mk_pages *p, int layer, const void *q
     if (qkv_stride < (long long)(n_heads + 2 * p->n_kv_heads) * d || qkv_stride % 8 ||
         q_stride < (long long)n_heads * d || q_stride % 8)
         return pages_refuse(who, "a stride is shorter than a row or not a multiple of 8");
+    // q in place of qkv's own q heads is fine: the lanes that write a value are those that read it, before
+    const bool in_place = q == qkv && qkv_dtype == p->dtype && q_stride == qkv_stride;
+    const size_t wide = qkv_dtype == MK_FP32 ? 4 : 2;
+    if (!in_place && pages_rows_meet(qkv, (size_t)(n_heads + 2 * p->n_kv_heads) * d * wide, (size_t)qkv_stride * wide, q,
+                                     (size_t)n_heads * d * 2, (size_t)q_stride * 2, (size_t)n * T))
+        return pages_refuse(who, "q must not overlap qkv, other than in place of its q heads");
     if (!(theta > 0.0) || !(eps >= 0.f)) return pages_refuse(who, "theta must be positive and eps not negative");
     RopeArgs a{*p, qkv, seqs, n_new, depth, static_cast<const uint16_t *>(q_gain),
                static_cast<const uint16_t *>(k_gain), static_cast<uint16_t *>(q), qkv_stride, q_stride,
