@@ -169,6 +169,38 @@ def test_a_pool_of_hundreds_of_thousands_of_pages():
         cache.check()
 
 
+def test_copies_in_large_pools_at_once():
+    """Four threads, each with a pool of its own size and a stream: no call
+    changes what another's launch needs."""
+    import threading
+
+    import tile_synchronised_b200 as mk
+    lib, failed = mk.load(), []
+
+    def work(n):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                kv = torch.zeros((2, 1, n, 1, 16, 64), dtype=torch.bfloat16, device="cuda")
+                kv[:, :, :8] = torch.arange(1, 9, device="cuda")[None, None, :, None, None, None].to(kv.dtype)
+                cache = mk.PagedCache.over(kv, ints([[-1]]), ints([0]), torch.zeros(n, dtype=torch.int32, device="cuda"))
+                src, dst = ints(list(range(8))), ints(list(range(n - 8, n)))
+                args = (cache._ref, cache._ref, src.data_ptr(), dst.data_ptr(), 8, stream.cuda_stream)
+                bad = sum(lib.mk_pages_copy(*args) != 0 for _ in range(10000))
+                cache.check()
+                assert bad == 0, f"{bad} calls failed"
+                assert torch.equal(kv[:, :, n - 8:], kv[:, :, :8])
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(n,)) for n in (1 << 19, 200_000, 400_000, 250_000)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+
+
 # ------------------------------------------------------------------ norm + rotation + append
 ROPE = [(8, 149 + (i % 3), *heads, d, dtype, src, bool(i & 1), bool(i & 2))
         for i, (d, dtype, src, heads) in enumerate(

@@ -22,6 +22,7 @@
 
 #include "mk_kernel.h"
 #include "mk_pages.h"
+#include "mk_tc.cuh"
 
 namespace mk {
 
@@ -588,8 +589,11 @@ extern "C" mk_status mk_pages_copy(const mk_pages *dst, const mk_pages *src, con
     if (n == 0) return MK_OK;
     const int smem = 2 * ((dst->n_pages + 31) / 32) * 4;
     if (smem > 48 * 1024) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(pages_copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        // raised to the largest pool's at once: raised to this pool's, another thread's call could lower it again
+        // before the launch
+        static std::atomic<unsigned long long> configured{0};
+        const cudaError_t e = tc_allow_smem(reinterpret_cast<const void *>(pages_copy_kernel),
+                                            2 * (kPagesMaxPages / 32) * 4, configured);
         if (e != cudaSuccess) return pages_launched(e, "pages_copy");
     }
     const long long bytes = (long long)dst->n_kv_heads * dst->page_size * dst->head_dim * 2;
