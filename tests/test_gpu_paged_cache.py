@@ -533,3 +533,69 @@ def test_q_in_place_and_between_the_rows_of_qkv(n, T):
     assert torch.equal(over, o)
     with pytest.raises(mk.MkError, match="overlap"):
         mk.attention_tree(between, a, 0, seqs, out=hold[..., width - 8:-8].view(n, T, nq, d))
+
+
+def test_tensors_dropped_behind_a_call_on_another_stream():
+    """While the other stream has not run the call yet, memory of its tensors
+    is not given to others."""
+    import tile_synchronised_b200 as mk
+    n, T, nq, nkv, d = 2, 600, 32, 2, 64
+    pool = filled([20, 33], [T, T], nkv=nkv, d=d, spare=2, seed=40, poison=False)
+    cache = pool.to_cache()
+    side = torch.cuda.Stream()
+    seqs, zero = ints(0, 1), ints(0, 0)
+    qkv = torch.randn((n, T, (nq + 2 * nkv) * d), generator=generator(41)).to(torch.bfloat16)
+    ref = mk.qk_norm_rope(qkv.cuda(), cache, 0, seqs, nq, 10000.0)
+    att = mk.attention_tree(ref, cache, 0, seqs)
+    warm = pool.to_cache()  # a kernel's first launch may wait for the device
+    warm.reserve(seqs, zero)
+    warm.compact(seqs, zero)
+    warm.free(seqs)
+    torch.cuda.synchronize()
+
+    def dropped(make, call):
+        x = make()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100_000_000)  # some 50 ms
+        got, at = call(x), x.data_ptr()
+        del x
+        others = [make() for _ in range(3)]
+        assert not side.query()
+        assert all(o.data_ptr() != at for o in others)
+        side.synchronize()
+        return got
+
+    qkv = qkv.cuda()
+    assert torch.equal(dropped(lambda: qkv.clone(), lambda x: mk.qk_norm_rope(x, cache, 0, seqs, nq, 10000.0, stream=side)), ref)
+    assert torch.equal(dropped(lambda: ref.clone(), lambda x: mk.attention_tree(x, cache, 0, seqs, stream=side)), att)
+    dropped(lambda: zero.clone(), lambda x: cache.reserve(seqs, x, stream=side))
+    dropped(lambda: zero.clone(), lambda x: cache.compact(seqs, x, stream=side))
+    cut = ints(20, 20)
+    dropped(lambda: cut.clone(), lambda x: cache.free(seqs, x, stream=side))
+    cache.check()
+    assert cache.lengths.tolist() == [20, 20]
+
+
+def test_a_capture_on_a_stream_that_the_calls_are_given():
+    """Tensors made and dropped inside the capture."""
+    import tile_synchronised_b200 as mk
+    T, nq, nkv, d = 5, 4, 2, 64
+    pool = filled([20, 33], [T, T], nkv=nkv, d=d, spare=2, seed=42, poison=False)
+    a, b = pool.to_cache(), pool.to_cache()
+    qkv = torch.randn((2, T, (nq + 2 * nkv) * d), generator=generator(43)).cuda()
+    seqs = ints(0, 1)
+    ref = mk.attention_tree(mk.qk_norm_rope(qkv, a, 0, seqs, nq, 10000.0), a, 0, seqs)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        q = mk.qk_norm_rope(qkv * 1.0, b, 0, seqs, nq, 10000.0, stream=side)
+        out = mk.attention_tree(q, b, 0, seqs, stream=side)
+        del q
+        b.compact(seqs, seqs + 1, stream=side)
+    for _ in range(2):
+        b.lengths.copy_(a.lengths)
+        out.zero_()
+        graph.replay()
+        b.check()
+        assert torch.equal(out, ref) and b.lengths.tolist() == [21, 35]

@@ -12,6 +12,10 @@ One step with drafted tokens:
 
 Lists (seqs, counts, ...) are int32 CUDA tensors; they are read when the
 kernels run, so a captured step follows their contents.
+
+Calls run on the current stream, or on `stream`.  There they are not ordered
+with what the current stream does, and a result that they allocate is that
+stream's; the tensors that they are given may be dropped at once.
 """
 from __future__ import annotations
 
@@ -46,6 +50,15 @@ def _elsewhere(device: torch.device, stream) -> bool:
 def _on(device: torch.device, stream):
     """The context of such a call: allocations made inside belong to its stream."""
     return torch.cuda.stream(torch.cuda.current_stream(device) if stream is None else stream)
+
+
+def _lend(stream, cache: "PagedCache", *tensors) -> None:
+    """For a call on a stream that it was given: the memory it uses stays what
+    it is until that stream is done with it, also if the caller drops it."""
+    if stream is not None:
+        for t in (cache.kv, cache.table, cache.lengths, cache.refs, cache._state, *tensors):
+            if t is not None:
+                t.record_stream(stream)
 
 
 def _ints(t, name: str, shape: tuple, index: int):
@@ -139,11 +152,13 @@ class PagedCache:
         """Room for counts[i] new tokens of sequence seqs[i], in pages it holds alone."""
         n = seqs.numel()
         self._call("mk_pages_reserve", stream, self._list("seqs", seqs, n), self._list("counts", counts, n), n)
+        _lend(stream, self, seqs, counts)
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
         """Empty sequence dst[i] shares the pages of src[i]'s committed positions."""
         n = src.numel()
         self._call("mk_pages_fork", stream, self._list("src", src, n), self._list("dst", dst, n), n)
+        _lend(stream, self, src, dst)
 
     def compact(self, seqs: torch.Tensor, n_keep: torch.Tensor, keep: torch.Tensor | None = None, stream=None) -> None:
         """Commit n_keep[i] new tokens of sequence seqs[i]: those at the
@@ -152,12 +167,14 @@ class PagedCache:
         width = 0 if keep is None else keep.shape[-1]
         self._call("mk_pages_compact", stream, self._list("seqs", seqs, n), self._list("n_keep", n_keep, n),
                    _ints(keep, "keep", (n, width), self._index), width, n)
+        _lend(stream, self, seqs, n_keep, keep)
 
     def free(self, seqs: torch.Tensor, lengths: torch.Tensor | None = None, stream=None) -> None:
         """Cut sequence seqs[i] to lengths[i] positions (0 by default) and give up the pages behind."""
         n = seqs.numel()
         self._call("mk_pages_free", stream, self._list("seqs", seqs, n),
                    None if lengths is None else self._list("lengths", lengths, n), n)
+        _lend(stream, self, seqs, lengths)
 
     def copy(self, src_pages: torch.Tensor, dst_pages: torch.Tensor, source: "PagedCache | None" = None,
              stream=None) -> None:
@@ -169,6 +186,7 @@ class PagedCache:
             raise ValueError("the two caches must be on the same device")
         self._call("mk_pages_copy", stream, src._ref, self._list("src_pages", src_pages, n),
                    self._list("dst_pages", dst_pages, n), n)
+        _lend(stream, self, src_pages, dst_pages, src.kv, src._state)
 
     def check(self, stream=None) -> None:
         """Raise MkError for the first error the cache's kernels met since the
@@ -243,7 +261,9 @@ def qk_norm_rope(qkv: torch.Tensor, cache: PagedCache, layer: int, seqs: torch.T
             raise ValueError("gains must be contiguous bf16 [head_dim]")
     if _elsewhere(dev, stream):
         with _on(dev, stream):
-            return qk_norm_rope(qkv, cache, layer, seqs, n_heads, theta, q_gain, k_gain, eps, n_new, depth, out)
+            got = qk_norm_rope(qkv, cache, layer, seqs, n_heads, theta, q_gain, k_gain, eps, n_new, depth, out)
+        _lend(stream, cache, qkv, seqs, q_gain, k_gain, n_new, depth, out)
+        return got
     if out is None:
         out = torch.empty((n, T, n_heads, d), dtype=cache.dtype, device=dev)
     st = cache.lib.mk_qk_norm_rope(
@@ -275,7 +295,9 @@ def attention_tree(q: torch.Tensor, cache: PagedCache, layer: int, seqs: torch.T
     stride = _tokens(q, "q", shape, types, at, nq * d)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
-            return attention_tree(q, cache, layer, seqs, n_new, mask, out, scratch)
+            got = attention_tree(q, cache, layer, seqs, n_new, mask, out, scratch)
+        _lend(stream, cache, q, seqs, n_new, mask, out, scratch)
+        return got
     if out is None:
         out = torch.empty(shape, dtype=cache.dtype, device=dev)
     elif out.data_ptr() == q.data_ptr():
