@@ -379,3 +379,25 @@ def test_a_long_sequence_with_a_missing_page():
     with pytest.raises(mk.MkError, match="no page"):
         cache.check()
     assert torch.isnan(got[0, 300:]).all() and torch.equal(got[0, :256], good[0, :256])
+
+
+def test_no_new_token_in_any_entry():
+    pool, q, _ = make([40, 0, 300], 5, 4, 2, 128, 16, torch.bfloat16, 65)
+    run_and_compare(pool, q, [2, 0, 1], [0, 0, 0], None)
+
+
+def test_two_calls_at_once_on_one_cache():
+    """Two streams, scratch of their own, other sequences: the bits of one
+    call after the other."""
+    import tile_synchronised_b200 as mk
+    pool, q, new = make([2000 - 60 * i for i in range(16)], 9, 16, 4, 128, 32, torch.bfloat16, 66)
+    cache = pool.to_cache()
+    qd, halves = q.cuda(), [torch.arange(a, a + 8, dtype=torch.int32).cuda() for a in (0, 8)]
+    one = [mk.attention_tree(qd[8 * h:8 * h + 8], cache, 0, halves[h]) for h in (0, 1)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [mk.attention_tree(qd[8 * h:8 * h + 8], cache, 0, halves[h], stream=streams[h]) for h in (0, 1)]
+        torch.cuda.synchronize()
+        cache.check()
+        assert torch.equal(got[0], one[0]) and torch.equal(got[1], one[1])

@@ -9,13 +9,16 @@
 //
 // The T new tokens of the G = nq / nkv query heads that share a KV head are
 // the rows of one matrix (row r = t G + g), the tokens that fit 128 rows the M of
-// an MMA, so the cache is read once for up to 256 rows and the arithmetic (4 d flops per row
-// and position) stays behind the memory traffic (4 d bytes per position).  Per
+// an MMA, and the cache is read once for up to 256 rows (128 at d = 256).  Few
+// rows are bound by that reading: 4 d bytes per position.  At 256 rows the 4 d
+// flops per row and position take nearly as long on the tensor cores, the
+// exponentials too, and the chain from one to the other twice that: 64 drafts at 3k to 4k
+// positions keep HBM at 0.49 and the tensor pipe at 0.40 of their rates.  Per
 // tile of NT positions:
 //     S = Q K^T  (tensor memory, M = 128, N = NT), softmax in registers,
 //     P (16 bit, tensor memory, over S) and O += P V (tensor memory, N = d).
 // One thread owns one row of S, so the running maximum and sum need no
-// exchange.  It holds 32 or 64 of the scores at a time: with more in registers
+// exchange.  It holds 64 of the scores at a time: with more in registers
 // the compiler spills, and with 227 KB of the SM given to the operands there is
 // hardly an L1 to spill to (scores all in registers: 2.4 times slower).  O is
 // rescaled only when the maximum grew by more than 2^8 since the last rescale:
@@ -46,11 +49,15 @@
 // to 235 us (exponentials and MMAs 2048 cycles each per tile of 256 rows, the
 // chain through both some 4000), 8 trees of 27 28 to 30 us, d = 256 trees 20 us,
 // chunks of 500 tokens 31 to 35 us, one small tree 12 us: of the last four
-// some 6 us pass before the first S and some 8 after the last P V.
+// some 6 us pass before the first S and some 8 after the last P V.  A chunk of
+// 4096 tokens behind 4096 at d = 128, 32 heads over 8: 520 us, 793 TFLOP/s, 0.57
+// of the rate that a matrix product keeps up; at d = 64 434 us, 476 TFLOP/s.
 //
 // P is rounded to the cache's 16-bit type (2^-8 relative at most in bf16, each
-// element on its own, as V's own storage); S, the maximum, the sum, O and the
-// records are 32 bits.
+// element on its own): both operands of an MMA have one type, and P in two parts
+// would double the MMAs and the stores of P V.  Against 64 bits results are off by
+// 2.3 parts in 1000 with it in bf16, 1.7 with P in 32 bits (the rounding of the
+// result itself).  S, the maximum, the sum, O and the records are 32 bits.
 #include <cuda.h>
 #include <math_constants.h>
 
@@ -1131,7 +1138,10 @@ static cudaError_t launch_tree(const CUtensorMap &mq, const CUtensorMap &mk, con
     attn_tree_kernel<D, BF16><<<grid, tree_threads(D), fixed + a.stages * stage, s>>>(mq, mk, mv, a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    // 8 rows a CTA, or 32 once 8 make more CTAs than run at the same time
+    // 8 rows a CTA, or 32 where 8 make more than 6 CTAs an SM.  The whole call with 8 and with 32, us, at 512 CTAs
+    // of 8 rows: d = 64 16.6 to 19.4 and 19.2 to 20.0, d = 128 22.2 to 24.8 and 20.9 to 25.1, d = 256 22.5 to 24.5
+    // and 22.9 to 24.5; at 128: 14.2 and 16.9, 14.8 and 18.7, 17.6 and 23.3; at 1024: 20.3 to 28.9 and 18.0 to 26.0,
+    // 29.9 to 41.4 and 20.5 to 32.1, 29.7 to 43.6 and 21.2 to 33.8.
     const int item = tree_groups(D) * a.toks, rts = (a.T + item - 1) / item;
     const auto blocks = [&](int rows) { return (a.rows_cap + rows - 1) / rows; };
     constexpr int col_blocks = D / Combine<D>::kCols;
